@@ -352,6 +352,104 @@ int moe_expert_ffn_noalloc(const moe_experts* w, const void* x, int xdt, int T, 
  */
 int moe_ffn_trace_events(void* const* events);
 
+/* --------------------------------------- grouped products over plain weights */
+
+/*
+ * Matrix products grouped by expert, over weights in plain row-major form: what training the expert
+ * matrices needs (forward, gradient of the rows, gradient of the weights), beside moe_expert_ffn, which
+ * runs packed experts forward.  Grouped rows p in [offsets[e], offsets[e+1]) belong to expert e (offsets
+ * from moe_permute, any row counts, zero included); r(p) = perm_src[p] / k with perm_src, else p:
+ *   moe_grouped_gemm     y[p][n]     = sum_k x[r(p)][k] w[e][n][k]
+ *   moe_grouped_gemm_dx  dx[p][k]    = sum_n dy[p][n] w[e][n][k]
+ *   moe_grouped_gemm_dw  dw[e][n][k] = sum_p dy[p][n] x[r(p)][k]      (0 for an expert without rows)
+ * One dense product is the call with E = 1 and offsets = {0, rows}.  Gate and up are one matrix of
+ * N = 2I rows (gate first), so that y is the gu of moe_swiglu.
+ * Operands are all bf16 or all fp32 (dt); sums are held in fp32 and rounded once (nearest-even) to the
+ * result's type (bf16 or fp32, any dt).  No atomics: results are bitwise reproducible.
+ * Offsets are clamped to [0, rows], a group whose end lies before its start is empty, and a perm_src
+ * entry that names no x row (outside [0, x_rows * k)) stands for a row of zeros.  Rows of y and dx at
+ * and past offsets[E] are left as they were.  Results must not overlap operands.
+ */
+typedef struct {
+  int rows;                /* grouped rows there is room for (T*k; offsets[E] of them are placed); <= 1<<24 */
+  int E, N, K;             /* experts (1..1024), output and input features (1..1<<20, any size) */
+  const int32_t* offsets;  /* device [E+1] */
+  const int32_t* perm_src; /* device [rows], or NULL: x is already in grouped order ([rows][K]) */
+  int k, x_rows;           /* with perm_src: its divisor (1..16) and the rows of x; ignored otherwise */
+  int64_t ldx, ldy, ldw;   /* elements between rows of x (dx), y (dy) and w (dw); 0: contiguous */
+  int64_t w_stride;        /* elements between experts of w (dw); 0: N * (ldw or K) */
+} moe_grouped;
+
+/* Workspace bytes the three products below need (device, 256-byte aligned; the largest of the three,
+ * 0 when none): partial sums of weight gradients with few tiles.  One call at a time may use it. */
+size_t moe_grouped_workspace(int dt, int rows, int N, int K, int E);
+
+/*
+ *   x  device [x_rows or rows][K], w device [E][N][K], y / dy device [rows][N], dx device [rows][K],
+ *   dw device [E][N][K]; dt: element type of the operands; ydt, dxdt, dwdt: of the result.
+ * Any element-aligned pointer and any row stride works; rows that start on 16-byte boundaries (K and N
+ * multiples of 8 in bf16, of 4 in fp32) take the direct loads.
+ * moe_grouped_gemm_dx ignores perm_src: dx has one row per grouped row (moe_combine with gate weights 1
+ * sums a token's rows).
+ * Errors: MOE_ERR_INVALID (null pointers, bad types, sizes or strides out of range, pointers that are
+ * not element-aligned), MOE_ERR_UNSUPPORTED (more result tiles than one launch can hold), MOE_ERR_WORKSPACE.
+ */
+int moe_grouped_gemm(const moe_grouped* g, int dt, const void* x, const void* w, void* y, int ydt, void* ws,
+                     size_t ws_bytes, void* stream);
+int moe_grouped_gemm_dx(const moe_grouped* g, int dt, const void* dy, const void* w, void* dx, int dxdt, void* ws,
+                        size_t ws_bytes, void* stream);
+int moe_grouped_gemm_dw(const moe_grouped* g, int dt, const void* dy, const void* x, void* dw, int dwdt, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* ------------------------------------------- 8-bit integer experts (W8A8) */
+
+/* what moe_quant_rows does to a row before it is quantized */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+
+/*
+ * Symmetric 8-bit quantization with one scale per row -- a token of activations, an output channel of
+ * weights (viewed as [E*N][K]):
+ *   v = x[r] (MOE_ACT_NONE, x [rows][K]), or SiLU(x[r][0..K)) * x[r][K..2K) (MOE_ACT_SWIGLU, x [rows][2K]),
+ *   scale[r] = max |v| / 127,  q[r][j] = the integer nearest to 127 v[j] / max |v| (halves to even).
+ * A row of zeros gets scale 0 and zeros.  A row that holds a NaN or an infinity gets scale NaN and zeros:
+ * every product with it is NaN, other rows are not touched.
+ *   x device, element type xdt; q device [rows][K] int8 (out); scale device [rows] fp32 (out)
+ *   n_rows  device, one int32: only rows below it are read and written (offsets + E: the placed rows);
+ *           NULL: all rows
+ * Errors: MOE_ERR_INVALID (null pointers, bad type or act, rows < 0, K out of 1..1<<20, pointers that are
+ * not element-aligned).
+ */
+int moe_quant_rows(const void* x, int xdt, int rows, int K, int act, const int32_t* n_rows, int8_t* q, float* scale,
+                   void* stream);
+
+/*
+ * The grouped product in 8-bit integers: y[p][n] = q_scale[r(p)] * w_scale[e][n] * sum_k q[r(p)][k] w[e][n][k],
+ * the sum exact in int32, the scales applied in fp32, one rounding to ydt (bf16 or fp32).
+ *   g: as above, strides in int8 elements (ldx of q, ldw and w_stride of w; ldy of y);  K <= 131071, for
+ *      which no sum of products of int8 values overflows
+ *   q device [x_rows or rows][K] int8, q_scale device [x_rows or rows] fp32, w device [E][N][K] int8,
+ *   w_scale device [E][N] fp32, y device [rows][N] (out)
+ * Errors: as moe_grouped_gemm; MOE_ERR_UNSUPPORTED for K > 131071.
+ */
+int moe_grouped_gemm_i8(const moe_grouped* g, const int8_t* q, const float* q_scale, const int8_t* w,
+                        const float* w_scale, void* y, int ydt, void* stream);
+
+/* ------------------------------------------------------- SwiGLU and gradient */
+
+/*
+ * The gate between an expert's two products, and its gradient, over rows gu = [g | u] of 2I elements:
+ *   moe_swiglu       h = SiLU(g) u
+ *   moe_swiglu_grad  dgu = [dh u s (1 + g (1 - s)) | dh g s],  s = 1 / (1 + e^-g);  and h again unless
+ *                    h is NULL (so that a forward pass need not keep it)
+ * fp32 arithmetic, one rounding to the type dt that all of them have.
+ *   gu, dgu device [rows][2I]; h, dh device [rows][I]; n_rows as in moe_quant_rows
+ * Errors: MOE_ERR_INVALID (null pointers, bad type, rows < 0, I out of 1..1<<20, pointers that are not
+ * element-aligned).
+ */
+int moe_swiglu(const void* gu, int dt, int rows, int I, const int32_t* n_rows, void* h, void* stream);
+int moe_swiglu_grad(const void* gu, const void* dh, int dt, int rows, int I, const int32_t* n_rows, void* dgu,
+                    void* h, void* stream);
+
 /* ------------------------------------------------------------------ combine */
 
 /*
@@ -365,6 +463,26 @@ int moe_ffn_trace_events(void* const* events);
  */
 int moe_combine(const float* y_perm, const float* topk_w, const int32_t* inv_perm, int T, int k, int H,
                 const float* shared_y, void* out, int odt, void* stream);
+
+/*
+ * Gradient of moe_combine with respect to the expert outputs, the gate weights and the router logits
+ * behind them, given the gradient dout of out (the shared expert's gradient is dout itself):
+ *   dy_perm[inv_perm[t*k+j]] = topk_w[t][j] * dout[t]                     (rounded once to ydt)
+ *   dtopk_w[t][j]            = sum_h dout[t][h] * y_perm[inv_perm[t*k+j]][h]
+ *   dlogits[t][e]            = sum over j with topk_ids[t][j] = e of
+ *                              topk_w[t][j] * (dtopk_w[t][j] - sum_i topk_w[t][i] * dtopk_w[t][i]), else 0
+ * (the last: gate weights that are the softmax of the chosen logits, as moe_route's are).  A dropped pair
+ * (inv_perm outside [0, T*k)) has dtopk_w 0, no part in dlogits, and no row of dy_perm; rows of dy_perm that no
+ * pair names are left as they were.
+ *   dout device [T][H] of type odt; y_perm device [T*k][H] fp32; dy_perm device [T*k][H] of type ydt (out);
+ *   dtopk_w device [T][k] fp32 (out); topk_ids device [T][k] int32 and dlogits device [T][E] fp32 (out),
+ *   or both NULL
+ * fp32 sums in a fixed order.  Errors: MOE_ERR_INVALID (null pointers, bad types, sizes out of range
+ * (E out of 1..1024 with dlogits), dlogits without topk_ids, pointers that are not element-aligned).
+ */
+int moe_combine_grad(const void* dout, int odt, const float* y_perm, const float* topk_w, const int32_t* inv_perm,
+                     int T, int k, int H, void* dy_perm, int ydt, float* dtopk_w, const int32_t* topk_ids, int E,
+                     float* dlogits, void* stream);
 
 /* -------------------------------------------------------------- expert cache */
 

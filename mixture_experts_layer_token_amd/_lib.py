@@ -21,6 +21,12 @@ class MoeExperts(ctypes.Structure):
                 ("pkg_stride", c_size_t), ("slot_of_expert", vp), ("n_slots", c_int)]
 
 
+class MoeGrouped(ctypes.Structure):
+    _fields_ = [("rows", c_int), ("E", c_int), ("N", c_int), ("K", c_int), ("offsets", vp), ("perm_src", vp),
+                ("k", c_int), ("x_rows", c_int), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("w_stride", ctypes.c_int64)]
+
+
 # moe_copy_fn: int (*)(void* ctx, void* dst, const void* src, size_t bytes, void* stream)
 COPY_FN = ctypes.CFUNCTYPE(c_int, vp, vp, vp, c_size_t, vp)
 
@@ -67,6 +73,16 @@ SIGNATURES = {
     "moe_expert_ffn_noalloc": ([ctypes.POINTER(MoeExperts), vp, c_int, c_int, c_int, i32p, i32p, f32p, c_int, vp],
                                c_int),
     "moe_ffn_trace_events": ([vp], c_int),
+    "moe_grouped_workspace": ([c_int, c_int, c_int, c_int, c_int], c_size_t),
+    "moe_grouped_gemm": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
+    "moe_grouped_gemm_dx": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
+    "moe_grouped_gemm_dw": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
+    "moe_grouped_gemm_i8": ([ctypes.POINTER(MoeGrouped), vp, f32p, vp, f32p, vp, c_int, vp], c_int),
+    "moe_quant_rows": ([vp, c_int, c_int, c_int, c_int, i32p, vp, f32p, vp], c_int),
+    "moe_swiglu": ([vp, c_int, c_int, c_int, i32p, vp, vp], c_int),
+    "moe_swiglu_grad": ([vp, vp, c_int, c_int, c_int, i32p, vp, vp, vp], c_int),
+    "moe_combine_grad": ([vp, c_int, f32p, f32p, i32p, c_int, c_int, c_int, vp, c_int, f32p, i32p, c_int, f32p, vp],
+                         c_int),
     "moe_combine": ([f32p, f32p, i32p, c_int, c_int, c_int, f32p, vp, c_int, vp], c_int),
     "moe_cache_create": ([ctypes.POINTER(MoeCacheDesc), ctypes.POINTER(vp)], c_int),
     "moe_cache_plan": ([vp, c_int, i32p, c_int, ctypes.POINTER(MoeCachePlan)], c_int),

@@ -12,11 +12,12 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import COPY_FN, MoeCacheDesc, MoeCachePlan, MoeCacheStats, MoeExperts, check, lib
+from ._lib import COPY_FN, MoeCacheDesc, MoeCachePlan, MoeCacheStats, MoeExperts, MoeGrouped, check, lib
 
 FMT = {"f32": 0, "bf16": 1, "mxfp4": 2, "int4g32": 3}
 DT = {"f32": 0, "bf16": 1}
 MODE = {"auto": 0, "decode": 1, "prefill": 2, "decode_mx": 3}
+ACT = {"none": 0, "swiglu": 1}
 POLICY = {"lru": 0, "lfu_decay": 1}
 TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
@@ -198,10 +199,177 @@ def moe_expert_ffn_noalloc(desc: MoeExperts, x, k, offsets, perm_src, y_perm, mo
                                        _dp(y_perm), MODE[mode], _stream(stream)))
 
 
+def moe_grouped_workspace(dt, rows, N, K, E) -> int:
+    return int(lib().moe_grouped_workspace(DT[dt], rows, N, K, E))
+
+
+def _rowp(t):
+    """Device pointer of a tensor whose last dimension is contiguous (rows may be strided)."""
+    assert t.is_cuda and (t.shape[-1] <= 1 or t.stride(-1) == 1), "expected a device tensor with contiguous rows"
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _step(t, dim):
+    """Elements between neighbours along `dim` (0, the default of the C call, where there is only one)."""
+    if t.shape[dim] <= 1:
+        return 0
+    if t.stride(dim) < 1:
+        raise ValueError("a tensor expanded along a dimension has no rows of its own")
+    return t.stride(dim)
+
+
+def _launch(f, args, tensors, stream):
+    """Call f(*args, stream) on the device that holds the tensors, whichever is current."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on %s and %s" % (dev, t.device))
+    if dev.index == torch.cuda.current_device():
+        check(f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            check(f(*args, _stream(stream)))
+
+
+def _grouped(x, w, y, offsets, perm_src, k) -> MoeGrouped:
+    """Descriptor of a grouped product: x [x_rows or rows, K] (dx), w [E, N, K] (dw), y [rows, N] (dy)."""
+    E, N, K = w.shape
+    if y.dim() != 2 or x.dim() != 2 or y.shape[1] != N or x.shape[1] != K:
+        raise ValueError("grouped product: x %s, w %s, y %s" % (tuple(x.shape), tuple(w.shape), tuple(y.shape)))
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise ValueError("offsets: %d int32 entries expected" % (E + 1))
+    rows = y.shape[0]
+    if perm_src is None:
+        if x.shape[0] != rows:
+            raise ValueError("x has %d rows, y %d (pass perm_src to gather)" % (x.shape[0], rows))
+    elif perm_src.dtype != torch.int32 or perm_src.numel() < rows:
+        raise ValueError("perm_src: %d int32 entries expected" % rows)
+    g = MoeGrouped()
+    g.rows, g.E, g.N, g.K = rows, E, N, K
+    g.offsets = _dp(offsets).value
+    g.perm_src = None if perm_src is None else _dp(perm_src).value
+    g.k, g.x_rows = k, x.shape[0]
+    g.ldx, g.ldy, g.ldw, g.w_stride = _step(x, 0), _step(y, 0), _step(w, 1), _step(w, 0)
+    return g
+
+
+def _same_dt(a, b):
+    if a.dtype != b.dtype:
+        raise TypeError("operands must have one type, got %s and %s" % (a.dtype, b.dtype))
+    return _dt(a)
+
+
+def _grouped_ws(ws, dt, g, device):
+    if ws is None:
+        need = int(lib().moe_grouped_workspace(dt, g.rows, g.N, g.K, g.E))
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return ws, _dp(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def moe_grouped_gemm(x, w, offsets, y, perm_src=None, k=1, ws=None, stream=None):
+    """y[p] = w[e] x[r(p)] for the rows p of every expert e.  `ws`: device workspace of at least
+    moe_grouped_workspace bytes (allocated here if None)."""
+    g, dt = _grouped(x, w, y, offsets, perm_src, k), _same_dt(x, w)
+    ws, wp, wn = _grouped_ws(ws, dt, g, x.device)
+    _launch(lib().moe_grouped_gemm, (ctypes.byref(g), dt, _rowp(x), _rowp(w), _rowp(y), _dt(y), wp, wn),
+            (x, w, y, offsets, perm_src, ws), stream)
+
+
+def moe_grouped_gemm_dx(dy, w, offsets, dx, ws=None, stream=None):
+    """dx[p] = w[e]^T dy[p]: the gradient of the grouped rows."""
+    g, dt = _grouped(dx, w, dy, offsets, None, 1), _same_dt(dy, w)
+    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device)
+    _launch(lib().moe_grouped_gemm_dx, (ctypes.byref(g), dt, _rowp(dy), _rowp(w), _rowp(dx), _dt(dx), wp, wn),
+            (dy, w, dx, offsets, ws), stream)
+
+
+def moe_grouped_gemm_dw(dy, x, offsets, dw, perm_src=None, k=1, ws=None, stream=None):
+    """dw[e] = sum over the rows p of expert e of dy[p] x[r(p)]^T: the gradient of the weights."""
+    g, dt = _grouped(x, dw, dy, offsets, perm_src, k), _same_dt(dy, x)
+    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device)
+    _launch(lib().moe_grouped_gemm_dw, (ctypes.byref(g), dt, _rowp(dy), _rowp(x), _rowp(dw), _dt(dw), wp, wn),
+            (dy, x, dw, offsets, perm_src, ws), stream)
+
+
+def _need(t, dtype, shape, what):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: %s %s expected, got %s %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    return t
+
+
+def _n_rows(n):
+    if n is not None and (n.dtype != torch.int32 or n.numel() != 1):
+        raise ValueError("n_rows: one int32 on the device expected")
+    return _dp(n)
+
+
+def moe_quant_rows(x, q, scale, act="none", n_rows=None, stream=None):
+    """8-bit rows and their scales: x [rows, K] (or [rows, 2K] = [g | u] with act="swiglu") -> q [rows, K] int8,
+    scale [rows] float32.  `n_rows`: device int32 (offsets[-1:]) that limits the rows."""
+    rows, K = q.shape
+    _need(x, x.dtype, (rows, 2 * K if act == "swiglu" else K), "x")
+    _need(q, torch.int8, (rows, K), "q")
+    _need(scale, torch.float32, (rows,), "scale")
+    _launch(lib().moe_quant_rows, (_dp(x), _dt(x), rows, K, ACT[act], _n_rows(n_rows), _dp(q), _dp(scale)),
+            (x, q, scale, n_rows), stream)
+
+
+def moe_grouped_gemm_i8(q, q_scale, w, w_scale, offsets, y, perm_src=None, k=1, stream=None):
+    """y[p] = q_scale[r(p)] * w_scale[e] * (w[e] q[r(p)]) with int8 q [.., K] and w [E, N, K]."""
+    g = _grouped(q, w, y, offsets, perm_src, k)
+    if q.dtype != torch.int8 or w.dtype != torch.int8:
+        raise TypeError("q and w must be int8, got %s and %s" % (q.dtype, w.dtype))
+    _need(q_scale, torch.float32, (q.shape[0],), "q_scale")
+    _need(w_scale, torch.float32, (g.E, g.N), "w_scale")
+    _launch(lib().moe_grouped_gemm_i8,
+            (ctypes.byref(g), _rowp(q), _dp(q_scale), _rowp(w), _dp(w_scale), _rowp(y), _dt(y)),
+            (q, q_scale, w, w_scale, y, offsets, perm_src), stream)
+
+
+def moe_swiglu(gu, h, n_rows=None, stream=None):
+    """h = SiLU(g) * u for rows gu = [g | u]."""
+    rows, I = h.shape
+    _need(gu, h.dtype, (rows, 2 * I), "gu")
+    _launch(lib().moe_swiglu, (_dp(gu), _dt(gu), rows, I, _n_rows(n_rows), _dp(h)), (gu, h, n_rows), stream)
+
+
+def moe_swiglu_grad(gu, dh, dgu, h=None, n_rows=None, stream=None):
+    """dgu = [dg | du] from gu and dh; `h`: optional tensor that takes SiLU(g) * u again."""
+    rows, I = dh.shape
+    _need(gu, dh.dtype, (rows, 2 * I), "gu")
+    _need(dgu, dh.dtype, (rows, 2 * I), "dgu")
+    if h is not None:
+        _need(h, dh.dtype, (rows, I), "h")
+    _launch(lib().moe_swiglu_grad, (_dp(gu), _dp(dh), _dt(gu), rows, I, _n_rows(n_rows), _dp(dgu), _dp(h)),
+            (gu, dh, dgu, h, n_rows), stream)
+
+
 def moe_combine(y_perm, topk_w, inv_perm, k, shared_y, out, stream=None):
     T, H = out.shape
     check(lib().moe_combine(_dp(y_perm), _dp(topk_w), _dp(inv_perm), T, k, H, _dp(shared_y), _dp(out), _dt(out),
                             _stream(stream)))
+
+
+def moe_combine_grad(dout, y_perm, topk_w, inv_perm, k, dy_perm, dtopk_w, topk_ids=None, dlogits=None, stream=None):
+    """Gradients of moe_combine: dy_perm [T*k, H], dtopk_w [T, k] and, with topk_ids and dlogits [T, E], of the
+    router logits."""
+    T, H = dout.shape
+    _need(y_perm, torch.float32, (T * k, H), "y_perm")
+    _need(dy_perm, dy_perm.dtype, (T * k, H), "dy_perm")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    _need(dtopk_w, torch.float32, (T, k), "dtopk_w")
+    if inv_perm.dtype != torch.int32 or inv_perm.numel() != T * k:
+        raise ValueError("inv_perm: %d int32 entries expected" % (T * k))
+    E = 0
+    if dlogits is not None:
+        E = dlogits.shape[1]
+        _need(dlogits, torch.float32, (T, E), "dlogits")
+        if topk_ids is not None:
+            _need(topk_ids, torch.int32, (T, k), "topk_ids")
+    _launch(lib().moe_combine_grad,
+            (_dp(dout), _dt(dout), _dp(y_perm), _dp(topk_w), _dp(inv_perm), T, k, H, _dp(dy_perm), _dt(dy_perm),
+             _dp(dtopk_w), _dp(topk_ids), E, _dp(dlogits)),
+            (dout, y_perm, topk_w, inv_perm, dy_perm, dtopk_w, topk_ids, dlogits), stream)
 
 
 class ExpertCache:
