@@ -32,9 +32,8 @@
 // next item's first blocks are loaded while the current item's results are written.
 #pragma once
 
-#include <utility>
-
 #include "ffn_common.hpp"
+#include "mfma_pipe.hpp"
 
 namespace moe {
 namespace {
@@ -107,32 +106,12 @@ __device__ __forceinline__ void mfma_acc(f32x4& acc, const f16x8& a, const f16x8
   else
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %2, %1, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ void acc_hazard_guard() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory"); }
-
 // An empty volatile asm that takes a value: the arithmetic producing it stays before this point
 // (the compiler would otherwise sink the decode next to the MFMA that reads it).
 __device__ __forceinline__ unsigned pin(unsigned x) {
   asm volatile("" : "+v"(x));
   return x;
 }
-
-// Compile-time loop: f(std::integral_constant<int, i>) for i = 0 .. N-1, so that every index is
-// a constant expression in the body (the K loop's schedule is decided while the code is written
-// out, not left to the unroller, which gives up on bodies this large).
-template <typename F, int... I>
-__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// n items spread over T slots, item i in slot i*T/n: the items of slot s are [spread_lo, spread_hi)
-constexpr int spread_lo(int s, int n, int T) { return (s * n + T - 1) / T; }
-constexpr int spread_hi(int s, int n, int T) { return ((s + 1) * n + T - 1) / T; }
-
-typedef const __attribute__((address_space(1))) char* gptr;
 
 // What every row-tile body needs: the work item and the matrix it multiplies.
 struct TileCtx {

@@ -50,9 +50,10 @@ __global__ __launch_bounds__(256) void simple_kernel(GroupArgs a) {
     const int2 r = group_range(a.offsets, e, a.rows);
     p0 = r.x, rows = r.y;
   } else {
-    const GroupTile t = find_group_tile(a.offsets, a.E, a.rows, kS, it0);
-    e = t.e, p0 = t.p0, rows = t.rows, i0 = 0;
-    if (e < 0) return;
+    const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, kS);
+    if (it0 >= sc.total) return;
+    const GroupSpan g = sc.find(a.offsets, a.E, a.rows, kS, it0);
+    e = g.e, p0 = g.p0 + (it0 - g.first) * kS, rows = min(kS, g.n - (it0 - g.first) * kS), i0 = 0;
   }
   const int ni = OP == kOpDw ? a.N - i0 : rows;            // results below and right of these do not exist
   const int nj = (OP == kOpY ? a.N : a.K) - j0;
@@ -132,6 +133,16 @@ __global__ __launch_bounds__(256) void simple_kernel(GroupArgs a) {
 size_t grouped_workspace(int, int, int, int, int) { return 0; }
 
 int launch_grouped(const GroupArgs& a, int op, int type, void*, hipStream_t s) {
+  // rows of the operands on 16-byte boundaries
+  const int eb = type == kI8 ? 1 : type == kBf16 ? 2 : 4;
+  auto al = [&](const void* p, long long ld) { return (uintptr_t)p % 16 == 0 && ld * eb % 16 == 0; };
+  const bool ax = op == kOpDx || (al(a.x, a.ldx) && a.K * eb % 16 == 0);
+  const bool aw = op == kOpDw || (al(a.w, a.ldw) && a.w_stride * eb % 16 == 0 && a.K * eb % 16 == 0);
+  const bool ay = op == kOpY || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
+  if (type != kF32 && ax && aw && ay) {
+    const int wi = 8;
+    return op == kOpY ? launch_tile_y(a, type, wi, s) : op == kOpDx ? launch_tile_dx(a, wi, s) : launch_tile_dw(a, wi, s);
+  }
   const int nj = op == kOpY ? a.N : a.K;
   const long long ty = op == kOpDw ? (long long)a.E * ((a.N + kS - 1) / kS) : group_tiles_max(a.rows, a.E, kS);
   if (ty == 0) return MOE_OK;

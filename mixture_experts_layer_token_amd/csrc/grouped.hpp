@@ -43,46 +43,47 @@ inline long long group_tiles_max(int rows, int E, int mr) {
   return (long long)rows / mr + (rows < E ? rows : E);
 }
 
-// Tile `slot` of the groups' row tiles.  Every wave of the workgroup computes it on its own (lane l
-// scans experts [l * per, (l + 1) * per)), so that it needs no LDS and no barrier; the result is uniform.
-// Returns e = -1 past the last tile; total = the number of tiles.
-struct GroupTile {
-  int e, p0, rows, total;
+// The groups' row tiles of mr rows in expert order.  Every wave scans the groups on its own (lane l takes experts
+// [l * per, (l + 1) * per)), so no LDS and no barrier is needed; totals and found tiles are uniform.
+struct GroupSpan {
+  int e, p0, n, first;  // expert, its first grouped row, its rows, its first tile
 };
-__device__ __forceinline__ GroupTile find_group_tile(const int32_t* __restrict__ offsets, int E, int rows, int mr,
-                                                     int slot) {
+struct GroupScan {
+  int acc, incl, total;  // this lane's tiles are [acc, incl); total of all lanes
+  // the group that tile `slot` (< total) belongs to
+  __device__ __forceinline__ GroupSpan find(const int32_t* __restrict__ offsets, int E, int rows, int mr,
+                                            int slot) const {
+    const int per = (E + 63) / 64, lane = threadIdx.x & 63;
+    GroupSpan f = {0, 0, 0, 0};
+    const bool mine = slot >= acc && slot < incl;
+    if (mine) {
+      int t = acc;
+      for (int e = lane * per; e < min(E, (lane + 1) * per); ++e) {
+        const int2 r = group_range(offsets, e, rows);
+        const int nt = (r.y + mr - 1) / mr;
+        if (slot >= t && slot < t + nt) f = GroupSpan{e, r.x, r.y, t};
+        t += nt;
+      }
+    }
+    const unsigned long long b = __ballot(mine);
+    const int owner = b ? __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(b)) : 0;
+    return GroupSpan{__builtin_amdgcn_readlane(f.e, owner), __builtin_amdgcn_readlane(f.p0, owner),
+                     __builtin_amdgcn_readlane(f.n, owner), __builtin_amdgcn_readlane(f.first, owner)};
+  }
+};
+__device__ __forceinline__ GroupScan scan_groups(const int32_t* __restrict__ offsets, int E, int rows, int mr) {
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) / 64;
-  const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
   int local = 0;
-  for (int e = e0; e < e1; ++e) local += (group_range(offsets, e, rows).y + mr - 1) / mr;
+  for (int e = lane * per; e < min(E, (lane + 1) * per); ++e)
+    local += (group_range(offsets, e, rows).y + mr - 1) / mr;
   int incl = local;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int t = __shfl_up(incl, off, 64);
     if (lane >= off) incl += t;
   }
-  int acc = incl - local, fe = -1, fp = 0, fr = 0;
-  const bool mine = slot >= acc && slot < incl;
-  if (mine)
-    for (int e = e0; e < e1; ++e) {
-      const int2 r = group_range(offsets, e, rows);
-      const int nt = (r.y + mr - 1) / mr;
-      if (fe < 0 && slot < acc + nt) {
-        fe = e;
-        fp = r.x + (slot - acc) * mr;
-        fr = min(mr, r.y - (slot - acc) * mr);
-      }
-      acc += nt;
-    }
-  const unsigned long long b = __ballot(mine);
-  const int owner = b ? __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(b)) : 0;
-  GroupTile t;
-  t.e = __builtin_amdgcn_readlane(fe, owner);
-  t.p0 = __builtin_amdgcn_readlane(fp, owner);
-  t.rows = __builtin_amdgcn_readlane(fr, owner);
-  t.total = __builtin_amdgcn_readlane(incl, 63);
-  return t;
+  return GroupScan{incl - local, incl, __builtin_amdgcn_readlane(incl, 63)};
 }
 
 __device__ __forceinline__ void store_out(void* out, size_t i, float v, int bf16) {
@@ -96,6 +97,10 @@ constexpr long long kMaxThreads = 0xFFFFFFFFLL;  // of one launch
 
 enum GroupType { kBf16 = 0, kF32 = 1, kI8 = 2 };
 
+// grouped_tile_*.hip: the MFMA tile kernel, rows and pointers on 16-byte boundaries
+int launch_tile_y(const GroupArgs& a, int type, int wi, hipStream_t s);
+int launch_tile_dx(const GroupArgs& a, int wi, hipStream_t s);
+int launch_tile_dw(const GroupArgs& a, int wi, hipStream_t s);
 // the kernel that suits the call; ws holds grouped_workspace bytes
 int launch_grouped(const GroupArgs& a, int op, int type, void* ws, hipStream_t s);
 size_t grouped_workspace(int type, int rows, int N, int K, int E);

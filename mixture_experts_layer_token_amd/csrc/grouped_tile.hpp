@@ -1,0 +1,478 @@
+// Tile kernel of the products grouped by expert over plain weights: C[i][j] = sum_c A[i][c] B[j][c] with both
+// operands in their row-major form, the output tile stationary in accumulation registers.
+//
+//   forward             i = grouped row,    j = output feature, c = input feature:  A, B contiguous along c
+//   gradient of rows    i = grouped row,    j = input feature,  c = output feature: B strided along c
+//   gradient of weights i = output feature, j = input feature,  c = grouped row:    A and B strided along c
+//
+// A workgroup of 4 waves (2 x 2) computes up to 32 WI x 32 WJ results of one expert; a wave owns 16 WI x 16 WJ of
+// them.  Bound by the matrix cores for many rows per expert, by the weights' bytes for few.
+//  - 4 stages of 64 bytes of c per row (32 bf16 or 64 int8) wait in LDS or on their way there, written by direct
+//    global->LDS loads of 16 bytes per lane; the fragments of the stage after the current one are read into
+//    registers while the current one is multiplied, so each buffer is free again one stage early and loads
+//    have three stages of time to land.  One barrier per stage; it leaves loads in flight.
+//  - an operand contiguous along c sits in LDS as rows of 64 bytes and is read as MFMA fragments directly
+//    (ds_read_b128); one that is strided along c sits there as it is in memory, c rows of up to 512 bytes, and is
+//    transposed on the way to the registers by ds_read_b64_tr_b16 (16 lanes read 4 rows of 16 elements,
+//    lane i receives column i), so neither needs a transposed copy in memory.  16-byte chunks (32-byte
+//    ones for the strided form) are XOR-swizzled by row against bank conflicts: the loads write LDS
+//    linearly, so the lanes fetch the chunks in swizzled order instead.
+//  - the B operand is the MFMA's first one: a lane's four results are four neighbouring columns j of one row i,
+//    stored as 8 or 16 bytes.
+//  - ragged rows: a group of n rows is cut into ceil(n / (32 WI)) tiles of even size, and a tile of r rows runs
+//    with NI = ceil(r / 32) row fragments per wave (the two wave rows take every other fragment).
+//  - a chunk past the end of c comes from a page of zeros on both sides (what lies behind a row may hold
+//    anything); rows and columns past the edge repeat valid ones and are not stored.
+#pragma once
+
+#include "grouped.hpp"
+#include "mfma_pipe.hpp"
+
+namespace moe {
+namespace {
+
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+
+template <int TYPE>
+struct TileT;
+template <>
+struct TileT<kBf16> {
+  typedef bf16x8 Frag;
+  typedef f32x4 Acc;
+  static constexpr int EB = 2;
+};
+template <>
+struct TileT<kI8> {
+  typedef i32x4 Frag;
+  typedef i32x4 Acc;
+  static constexpr int EB = 1;
+};
+
+// In-place MFMA on an accumulator held in AGPRs; b is the first operand (see the head of the file).  Its operands
+// come straight from LDS reads, which the compiler waits for; no vector instruction writes them.
+__device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+__device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x4& a) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
+typedef __attribute__((address_space(3))) char* lptr;
+constexpr int kDepth = 4;     // stages
+constexpr int kStageC = 64;   // bytes of c per row and stage
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ void lds_load16(gptr g, lptr l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+}
+
+// ------------------------------------------------------------------ operands
+// One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; F fragments
+// of 16 rows are read per wave.
+template <int BM, int EB>
+struct Contig {
+  static constexpr int LQ = BM / 64;
+  static constexpr int BYTES = BM * kStageC;
+  gptr ptr[LQ];
+  int inc[LQ];  // 0: a row of zeros
+  int c_byte;   // this lane's byte of c within a stage
+
+  static __device__ __forceinline__ int swz(int r) { return (r >> 1) & 3; }
+  // row(r): address of row r (its first byte), or null for a row of zeros
+  template <typename F>
+  __device__ __forceinline__ void init(int wave, int lane, F&& row) {
+    c_byte = ((lane & 3) ^ swz(lane >> 2)) * 16;
+#pragma unroll
+    for (int q = 0; q < LQ; ++q) {
+      const gptr p = row((q * kWaves + wave) * 16 + lane / 4);
+      inc[q] = p ? kStageC : 0;
+      ptr[q] = p ? p + c_byte : (gptr)g_zero_page;
+    }
+  }
+  // load q of the next stage; left: bytes of c from that stage's start to the end of the row (the comparison in every
+  // stage costs little beside its 16 WI WJ matrix instructions, and a second loop without it made the compiler
+  // copy accumulators between registers from loop to loop)
+  __device__ __forceinline__ void issue(int q, lptr lds, int wave, int left) {
+    const gptr p = c_byte >= left ? (gptr)g_zero_page : ptr[q];
+    lds_load16(p, lds + (q * kWaves + wave) * 1024);
+    ptr[q] += inc[q];
+  }
+  // fragment address of this lane: first row r0 (a multiple of 16)
+  static __device__ __forceinline__ int lane_addr(int r0, int lane) {
+    return (r0 + (lane & 15)) * kStageC + ((lane >> 4) ^ swz(lane & 15)) * 16;
+  }
+  template <typename Frag>
+  static __device__ __forceinline__ Frag read(lptr base, int addr, int f, int step16) {
+    return *(const __attribute__((address_space(3))) Frag*)(base + addr + f * step16 * 16 * kStageC);
+  }
+};
+
+// (bf16 only) BM columns of memory rows that are c; swizzled in 32-byte pairs of chunks
+template <int BM>
+struct Strided {
+  static constexpr int LQ = BM / 64;
+  static constexpr int BYTES = BM * kStageC;
+  static constexpr int RB = BM * 2;        // bytes per c row
+  static constexpr int RPL = 1024 / RB;    // c rows per wave-wide load
+  static constexpr int CPR = RB / 16;      // chunks per c row
+  gptr ptr[LQ];
+  long long inc;
+
+  static __device__ __forceinline__ int swz(int c) {
+    return BM >= 128 ? (c & 3) | ((c >> 3) & 1) << 2 : ((c >> 1) & 1) | ((c >> 3) & 1) << 1;
+  }
+  static __device__ __forceinline__ int c_row(int q, int wave, int lane) {
+    return (q * kWaves + wave) * RPL + lane / CPR;
+  }
+  // this lane's column of load q: `cols` exist
+  static __device__ __forceinline__ int col(int q, int wave, int lane, int cols) {
+    const int slot = lane % CPR, ch = (((slot >> 1) ^ swz(c_row(q, wave, lane))) << 1) | (slot & 1);
+    return ch * 8 < cols ? ch * 8 : 0;
+  }
+  __device__ __forceinline__ void init(int wave, int lane, gptr base, long long ld_bytes, int cols) {
+    inc = 32 * ld_bytes;
+#pragma unroll
+    for (int q = 0; q < LQ; ++q) ptr[q] = base + c_row(q, wave, lane) * ld_bytes + col(q, wave, lane, cols) * 2;
+  }
+  __device__ __forceinline__ void issue(int q, lptr lds, int wave, int lane, int left_rows) {
+    const gptr p = c_row(q, wave, lane) >= left_rows ? (gptr)g_zero_page : ptr[q];
+    lds_load16(p, lds + (q * kWaves + wave) * 1024);
+    ptr[q] += inc;
+  }
+  // lane i of each 16 reads c row 8 (lane / 16) + i / 4, four columns from 4 (i % 4); the second read takes the c
+  // rows 4 below.  m: index of the 16-column fragment.
+  static __device__ __forceinline__ int lane_addr(int m, int lane) {
+    const int c = 8 * (lane >> 4) + ((lane & 15) >> 2);
+    return c * RB + ((m ^ swz(c)) << 5) + 8 * (lane & 3);
+  }
+  // fragment m ^ x (x: the bits by which it differs from lane_addr's)
+  static __device__ __forceinline__ bf16x8 read(lptr base, int addr, int x) {
+    typedef __attribute__((address_space(3))) s16x4* p4;
+    const lptr p = base + (addr ^ (x << 5));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * RB));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// ------------------------------------------------------------------ tiles
+struct TileItem {
+  int e, i0, ni, j0, nj, p0, nc;  // expert; first i and j and how many exist; first grouped row; length of c
+};
+
+// Division of a grouped pair's flat index by k (2 <= k <= 16, index below 2^28): multiplication by ceil(2^32 / k),
+// off by less than 1 / k there.
+__device__ __forceinline__ int div_k(int s, int k, unsigned magic) { return k == 1 ? s : (int)__umulhi((unsigned)s, magic); }
+
+template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+struct TileKernel {
+  typedef TileT<TYPE> TT;
+  typedef typename TT::Frag Frag;
+  typedef typename TT::Acc Acc;
+  static constexpr int EB = TT::EB, KE = kStageC / EB;  // elements of c per stage
+  static constexpr int BI = 32 * WI, BJ = 32 * WJ;
+  static constexpr bool SA = OP == kOpDw, SB = OP != kOpY;  // strided operands
+  typedef typename std::conditional<SA, Strided<BI>, Contig<BI, EB>>::type OpA;
+  typedef typename std::conditional<SB, Strided<BJ>, Contig<BJ, EB>>::type OpB;
+  static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
+  static constexpr size_t LDS = (size_t)kDepth * STAGE;
+  static constexpr bool IDX = GATHER && OP == kOpDw;  // x rows of c through perm_src: one more load per stage
+  static constexpr int VPS = OpA::LQ + OpB::LQ + (IDX ? 1 : 0);  // vector-memory operations per stage and wave
+
+  // One tile with NI row fragments per wave.
+  template <int NI>
+  static __device__ __forceinline__ void body(const GroupArgs& a, const TileItem& t, lptr lds) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave >> 1, wj = wave & 1;
+    const unsigned magic = a.k > 1 ? (unsigned)((0x100000000ULL + a.k - 1) / a.k) : 0;
+
+    // ---- operands
+    OpA A;
+    OpB B;
+    const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
+    if constexpr (OP == kOpY) {
+      A.init(wave, lane, [&](int r) -> gptr {
+        const int p = t.p0 + min(r, t.ni - 1);
+        const int xr = x_row(a, p);
+        return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
+      });
+      B.init(wave, lane, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
+    } else if constexpr (OP == kOpDx) {
+      A.init(wave, lane, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
+      B.init(wave, lane, w + (size_t)t.j0 * EB, a.ldw * EB, t.nj);
+    } else {
+      A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.ni);
+      if constexpr (!IDX) B.init(wave, lane, x + ((size_t)t.p0 * a.ldx + t.j0) * EB, a.ldx * EB, t.nj);
+    }
+    // IDX: lane l holds the x row of c row 32 s + l % 32 of the next stage s to be loaded (-1: zeros)
+    int idx = -1, idx_next = -1;
+    int bcol[OpB::LQ];
+    auto idx_load = [&](int s) {
+      const int c = s * 32 + (lane & 31);
+      return c < t.nc ? a.perm_src[t.p0 + c] : -1;
+    };
+    auto idx_row = [&](int v) {
+      const int r = div_k(v, a.k, magic);
+      return v >= 0 && r < a.x_rows ? r : -1;
+    };
+    auto issue_b_gather = [&](int q, lptr l) {
+      if constexpr (IDX) {
+        int r = __builtin_amdgcn_readlane(idx, (q * kWaves + wave) * OpB::RPL);
+#pragma unroll
+        for (int i = 1; i < OpB::RPL; ++i) {
+          const int ri = __builtin_amdgcn_readlane(idx, (q * kWaves + wave) * OpB::RPL + i);
+          r = lane / OpB::CPR == i ? ri : r;
+        }
+        const gptr p = x + ((size_t)(unsigned)max(r, 0) * a.ldx + t.j0 + bcol[q]) * EB;
+        lds_load16(r >= 0 ? p : (gptr)g_zero_page, l + (q * kWaves + wave) * 1024);
+      }
+    };
+    if constexpr (IDX) {
+#pragma unroll
+      for (int q = 0; q < OpB::LQ; ++q) bcol[q] = OpB::col(q, wave, lane, t.nj);
+    }
+    // load L of stage s into its buffer
+    auto issue = [&](int L, int s, int buf) {
+      const lptr la = lds + buf * STAGE, lb = la + OpA::BYTES;
+      const int left = t.nc - s * KE;
+      if (L < OpA::LQ) {
+        if constexpr (SA) A.issue(L, la, wave, lane, left);
+        else A.issue(L, la, wave, left * EB);
+      } else {
+        if constexpr (IDX) issue_b_gather(L - OpA::LQ, lb);
+        else if constexpr (SB) B.issue(L - OpA::LQ, lb, wave, lane, left);
+        else B.issue(L - OpA::LQ, lb, wave, left * EB);
+      }
+    };
+    constexpr int NL = OpA::LQ + OpB::LQ;
+
+    // ---- fragments.  Row fragments of wave row wi: 2 f + wi; column fragments of wave column wj: WJ wj + f
+    int addr_a, addr_b;
+    if constexpr (SA) addr_a = OpA::lane_addr(wi, lane);
+    else addr_a = OpA::lane_addr(16 * wi, lane);
+    if constexpr (SB) addr_b = OpB::lane_addr(WJ * wj, lane);
+    else addr_b = OpB::lane_addr(16 * WJ * wj, lane);
+    auto read_a = [&](int f, int buf) -> Frag {
+      const lptr l = lds + buf * STAGE;
+      if constexpr (SA) return OpA::read(l, addr_a, 2 * f);
+      else return OpA::template read<Frag>(l, addr_a, f, 2);
+    };
+    auto read_b = [&](int f, int buf) -> Frag {
+      const lptr l = lds + buf * STAGE + OpA::BYTES;
+      if constexpr (SB) return OpB::read(l, addr_b, f);
+      else return OpB::template read<Frag>(l, addr_b, f, 1);
+    };
+
+    Acc acc[WJ][NI];
+#pragma unroll
+    for (int j = 0; j < WJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[j][i] = Acc{};
+
+    // ---- prologue: the first kDepth stages
+    const int ns = (t.nc + KE - 1) / KE;  // >= 1
+    {
+#pragma unroll
+      for (int s = 0; s < kDepth; ++s) {
+        if constexpr (IDX) idx = idx_row(idx_load(s));
+#pragma unroll
+        for (int L = 0; L < NL; ++L) issue(L, s, s);
+      }
+      if constexpr (IDX) idx_next = idx_load(kDepth);
+      Frag fa[2][NI], fb[2][WJ];
+      MOE_WAIT_VMCNT((kDepth - 1) * NL);  // (with IDX more are outstanding: the wait is stricter than needed)
+      barrier_keep_loads();
+#pragma unroll
+      for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0);
+#pragma unroll
+      for (int j = 0; j < WJ; ++j) fb[0][j] = read_b(j, 0);
+
+      // ---- one stage: at its start the barrier publishes stage s+1 (every wave has waited for its own loads of
+      // it) and frees the buffer of stage s (its fragments are in registers), which stage s+4 then fills
+      auto stage = [&](auto parity, int s) {
+        constexpr int cur = decltype(parity)::value, nxt = cur ^ 1;
+        MOE_WAIT_VMCNT((kDepth - 2) * VPS);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        barrier_keep_loads();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (IDX) {
+          idx = idx_row(idx_next);
+          idx_next = idx_load(s + kDepth + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const int rbuf = (s + 1) & (kDepth - 1), lbuf = s & (kDepth - 1);
+        constexpr int R = WJ * NI, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
+        static_for<R>([&](auto rc) {
+          constexpr int r = rc, j = r / NI, i = r % NI;
+          tile_mfma(acc[j][i], fb[cur][j], fa[cur][i]);
+          constexpr int lo = spread_lo(r, NR, T), hi = r < T ? spread_hi(r, NR, T) : lo;
+          static_for<hi - lo>([&](auto mc) {
+            constexpr int m = lo + mc;
+            if constexpr (m < NI) fa[nxt][m] = read_a(m, rbuf);
+            else fb[nxt][m - NI] = read_b(m - NI, rbuf);
+          });
+          constexpr int l0 = spread_lo(r, NL, R), l1 = spread_hi(r, NL, R);
+          static_for<l1 - l0>([&](auto Lc) { issue(l0 + Lc, s + kDepth, lbuf); });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      // (an odd number of stages ends with one over zeros)
+      int s = 0;
+      do {
+        stage(std::integral_constant<int, 0>{}, s);
+        stage(std::integral_constant<int, 1>{}, s + 1);
+        s += 2;
+      } while (s < ns);
+      __builtin_amdgcn_s_waitcnt(0);  // nothing may land in LDS once the workgroup is gone
+    }
+
+    // ---- results.  The accumulators pass an empty asm after the wait states, so that no read of them can be
+    // scheduled before.
+    acc_hazard_guard();
+#pragma unroll
+    for (int j = 0; j < WJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) asm volatile("" : "+a"(acc[j][i]));
+    const int q4 = (lane >> 4) * 4;
+    const long long ldc = OP == kOpY ? a.ldy : OP == kOpDx ? a.ldx : a.ldw;
+    const int ob = a.out_bf16 ? 2 : 4;
+    char* out = (char*)(OP == kOpY ? a.y : OP == kOpDx ? a.x : a.w);
+    out += (OP == kOpDw ? (size_t)t.e * a.w_stride + (size_t)t.i0 * ldc : (size_t)t.p0 * ldc) * ob;
+    const bool wide = ((size_t)out | (size_t)(ldc * ob)) % (4 * ob) == 0;  // rows start on a store's width
+    const int rlane = wi * 16 + (lane & 15);  // row of fragment 0; the others follow 32 rows apart
+    float rs[NI];
+    if constexpr (TYPE == kI8) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int xr = x_row(a, t.p0 + min(32 * i + rlane, t.ni - 1));
+        rs[i] = xr >= 0 ? a.x_scale[xr] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) {
+      const int jj = (WJ * wj + j) * 16 + q4, left = t.nj - jj;
+      if (left <= 0) continue;
+      const size_t col = (size_t)t.j0 + jj;
+      float sw[4];
+      if constexpr (TYPE == kI8) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sw[r] = a.w_scale[(size_t)t.e * a.N + t.j0 + min(jj + r, t.nj - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int ii = 32 * i + rlane;
+        if (ii >= t.ni) continue;
+        char* row = out + (size_t)ii * ldc * ob;
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (TYPE == kI8) v[r] = (float)acc[j][i][r] * rs[i] * sw[r];
+          else v[r] = acc[j][i][r];
+        }
+        if (wide && left >= 4) {
+          if (a.out_bf16)
+            *(u32x2*)(row + col * 2) = u32x2{(unsigned)f32_to_bf16_rne(v[0]) | ((unsigned)f32_to_bf16_rne(v[1]) << 16),
+                                             (unsigned)f32_to_bf16_rne(v[2]) | ((unsigned)f32_to_bf16_rne(v[3]) << 16)};
+          else
+            *(f32x4*)(row + col * 4) = v;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < left) store_out(row, col + r, v[r], a.out_bf16);
+        }
+      }
+    }
+  }
+};
+
+// Tiles in launch order: workgroup b runs on XCD b % 8, and each XCD takes a contiguous range of the tiles, so
+// that its L2 serves the operands its workgroups share.  Tiles of an expert go in bands of up to 8 row tiles,
+// column by column: the 32 tiles an XCD works on at a time span 8 row and 4 column panels.
+constexpr int kBand = 8;
+__device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, int& col) {
+  const int band = u / (kBand * ncol), r = u - band * kBand * ncol, h = min(kBand, nt - band * kBand);
+  col = r / h;
+  row = band * kBand + r - col * h;
+}
+
+template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+__global__ __launch_bounds__(256, (WI * WJ > 16 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER> Tk;
+  extern __shared__ __align__(1024) char smem[];
+  const int nj = OP == kOpY ? a.N : a.K, ncol = (nj + Tk::BJ - 1) / Tk::BJ;
+  TileItem t;
+  int row, col;
+  const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
+  if constexpr (OP == kOpDw) {
+    const int nt = (a.N + Tk::BI - 1) / Tk::BI;
+    const int per = (int)((gridDim.x + kXcds - 1) / kXcds);  // the grid is a multiple of the XCDs
+    const long long u = (long long)xcd * per + local;
+    if (u >= (long long)a.E * nt * ncol) return;
+    t.e = __builtin_amdgcn_readfirstlane((int)(u / ((long long)nt * ncol)));
+    band_order((int)(u - (long long)t.e * nt * ncol), nt, ncol, row, col);
+    const int2 g = group_range(a.offsets, t.e, a.rows);
+    t.p0 = g.x, t.nc = g.y;
+    t.i0 = row * Tk::BI;
+    t.ni = min(Tk::BI, a.N - t.i0);
+  } else {
+    const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, Tk::BI);
+    const int total = sc.total * ncol, per = (total + kXcds - 1) / kXcds;
+    if (local >= per || xcd * per + local >= total) return;
+    const int u = xcd * per + local;
+    const GroupSpan g = sc.find(a.offsets, a.E, a.rows, Tk::BI, u / ncol);
+    t.e = g.e;
+    const int nt = (g.n + Tk::BI - 1) / Tk::BI;
+    band_order(u - g.first * ncol, nt, ncol, row, col);
+    const int r0 = (int)((long long)row * g.n / nt), r1 = (int)((long long)(row + 1) * g.n / nt);
+    t.p0 = g.p0 + r0, t.ni = r1 - r0, t.i0 = 0;
+    t.nc = OP == kOpY ? a.K : a.N;
+  }
+  t.j0 = col * Tk::BJ;
+  t.nj = min(Tk::BJ, nj - t.j0);
+  // everything about the tile is uniform
+  t.i0 = __builtin_amdgcn_readfirstlane(t.i0), t.ni = __builtin_amdgcn_readfirstlane(t.ni);
+  t.j0 = __builtin_amdgcn_readfirstlane(t.j0), t.nj = __builtin_amdgcn_readfirstlane(t.nj);
+  t.p0 = __builtin_amdgcn_readfirstlane(t.p0), t.nc = __builtin_amdgcn_readfirstlane(t.nc);
+  if constexpr (OP == kOpDw) {
+    if (t.nc == 0) {  // an expert without rows
+      char* out = (char*)a.w + ((size_t)t.e * a.w_stride + (size_t)t.i0 * a.ldw + t.j0) * (a.out_bf16 ? 2 : 4);
+      for (int i = threadIdx.x / 64; i < t.ni; i += kWaves)
+        for (int j = threadIdx.x % 64; j < t.nj; j += 64) store_out(out, (size_t)i * a.ldw + j, 0.f, a.out_bf16);
+      return;
+    }
+  }
+  const int n = (t.ni + 31) / 32;
+  static_for<WI>([&](auto ic) {
+    constexpr int NI = ic + 1;
+    if (n == NI) Tk::template body<NI>(a, t, (lptr)smem);
+  });
+}
+
+template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+int tile_launch_one(const GroupArgs& a, hipStream_t s) {
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER> Tk;
+  static bool attr_set[64];  // per device
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (!attr_set[dev]) {
+    hipError_t e = hipFuncSetAttribute((const void*)grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)Tk::LDS);
+    if (e != hipSuccess) return hip_fail(e, "moe_grouped_gemm: LDS attribute");
+    attr_set[dev] = true;
+  }
+  const int nj = OP == kOpY ? a.N : a.K;
+  const long long nt = OP == kOpDw ? (long long)a.E * ((a.N + Tk::BI - 1) / Tk::BI) : group_tiles_max(a.rows, a.E, Tk::BI);
+  long long nb = nt * ((nj + Tk::BJ - 1) / Tk::BJ);
+  if (nb == 0) return MOE_OK;
+  nb = (nb + kXcds - 1) / kXcds * kXcds;
+  if (nb > kMaxThreads / 256) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
+  hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER>), dim3((unsigned)nb), dim3(256), Tk::LDS, s, a);
+  MOE_CHECK_LAUNCH("moe_grouped_gemm launch");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
