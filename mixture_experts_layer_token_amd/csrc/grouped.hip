@@ -139,7 +139,7 @@ int launch_grouped(const GroupArgs& a, int op, int type, void*, hipStream_t s) {
   const bool ax = op == kOpDx || (al(a.x, a.ldx) && a.K * eb % 16 == 0);
   const bool aw = op == kOpDw || (al(a.w, a.ldw) && a.w_stride * eb % 16 == 0 && a.K * eb % 16 == 0);
   const bool ay = op == kOpY || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
-  if (type != kF32 && ax && aw && ay) {
+  if (type != kF32 && ax && aw && ay && tile_spans_fit(a, op, eb)) {
     const int wi = 8;
     return op == kOpY ? launch_tile_y(a, type, wi, s) : op == kOpDx ? launch_tile_dx(a, wi, s) : launch_tile_dw(a, wi, s);
   }

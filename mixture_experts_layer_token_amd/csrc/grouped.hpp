@@ -97,6 +97,15 @@ constexpr long long kMaxThreads = 0xFFFFFFFFLL;  // of one launch
 
 enum GroupType { kBf16 = 0, kF32 = 1, kI8 = 2 };
 
+constexpr long long kMaxSpan = 0xFFFF0000LL;  // bytes a buffer descriptor of the tile kernel may cover
+// Whether every descriptor of the kernel covers its operand: rows of a tile, or all of x where it is gathered, within
+// 32-bit offsets.
+inline bool tile_spans_fit(const GroupArgs& a, int op, int eb) {
+  auto rows = [&](long long n, long long ld) { return (n - 1) * ld * eb + ld * eb <= kMaxSpan && ld * eb < kMaxSpan / 512; };
+  const bool x = a.perm_src ? a.x_rows == 0 || rows(a.x_rows, a.ldx) : rows(256, a.ldx);
+  return (op == kOpDx || x) && (op == kOpDw || rows(256, a.ldw)) && (op == kOpY || rows(256, a.ldy));
+}
+
 // grouped_tile_*.hip: the MFMA tile kernel, rows and pointers on 16-byte boundaries
 int launch_tile_y(const GroupArgs& a, int type, int wi, hipStream_t s);
 int launch_tile_dx(const GroupArgs& a, int wi, hipStream_t s);

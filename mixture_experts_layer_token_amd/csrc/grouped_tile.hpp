@@ -21,8 +21,8 @@
 //    stored as 8 or 16 bytes.
 //  - ragged rows: a group of n rows is cut into ceil(n / (32 WI)) tiles of even size, and a tile of r rows runs
 //    with NI = ceil(r / 32) row fragments per wave (the two wave rows take every other fragment).
-//  - a chunk past the end of c comes from a page of zeros on both sides (what lies behind a row may hold
-//    anything); rows and columns past the edge repeat valid ones and are not stored.
+//  - chunks past the end of c are zeros on both sides (what lies behind a row may hold anything); rows and
+//    columns past the edge repeat valid ones and are not stored.
 #pragma once
 
 #include "grouped.hpp"
@@ -49,6 +49,12 @@ struct TileT<kI8> {
   static constexpr int EB = 1;
 };
 
+// Waits until at most N of this wave's loads are in flight (the compiler does not know the ones in inline assembly)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
 // In-place MFMA on an accumulator held in AGPRs; b is the first operand (see the head of the file).  Its operands
 // come straight from LDS reads, which the compiler waits for; no vector instruction writes them.
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a) {
@@ -63,41 +69,71 @@ constexpr int kDepth = 4;     // stages
 constexpr int kStageC = 64;   // bytes of c per row and stage
 constexpr int kWaves = 4;
 
-__device__ __forceinline__ void lds_load16(gptr g, lptr l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+// ------------------------------------------------------------------ operands
+// Operands are read through buffer descriptors with an exact length: a lane whose offset lies past the end
+// gets zeros, which is how everything outside an operand (the end of c, rows of zeros) enters the LDS as
+// zeros with no work per load.  The base advances by scalar arithmetic, the lanes' 32-bit offsets stay.
+constexpr unsigned kOutside = 0xFFFFFC00u;      // offset past the end of every descriptor, also with a row's bytes added
+
+// The loads are inline assembly (they have no result register: the data goes to LDS): after the compiler's own
+// LDS-direct loads, every transposing LDS read would wait for all loads in flight.  `Load` is one of them, kept
+// until it is written out, on its own or around an MFMA, which then separates the write of m0 from its use.
+struct Load {
+  u32x4 desc;
+  unsigned voff, lds;
+};
+__device__ __forceinline__ Load make_load(gptr base, unsigned bytes, unsigned voff, lptr l) {
+  const unsigned long long p = (unsigned long long)base;
+  // (uniform already: this only keeps the compiler from holding them in vector registers)
+  auto u = [](unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); };
+  return Load{u32x4{u((unsigned)p), u((unsigned)(p >> 32)) & 0xFFFFu, u(bytes), 0x00027000u}, voff,
+              u((unsigned)(size_t)l)};
+}
+__device__ __forceinline__ void load_now(const Load& d) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               : : "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+}
+__device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a, const Load& d) {
+  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+               : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+}
+__device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x4& a, const Load& d) {
+  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+               : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
 
-// ------------------------------------------------------------------ operands
-// One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; F fragments
-// of 16 rows are read per wave.
+// One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; fragments
+// of 16 rows are read.
 template <int BM, int EB>
 struct Contig {
   static constexpr int LQ = BM / 64;
   static constexpr int BYTES = BM * kStageC;
-  gptr ptr[LQ];
-  int inc[LQ];  // 0: a row of zeros
-  int c_byte;   // this lane's byte of c within a stage
+  gptr base;          // first byte of the stage to be loaded next, row 0
+  unsigned span;      // bytes of the operand; the lanes that are not kOutside never pass its end
+  int left;           // bytes of c from there to the end of a row
+  unsigned voff[LQ];  // this lane's bytes
+  unsigned tail;      // its part of the next stage lies past the end of c: kOutside, else 0
+  int c_byte;         // its byte of c within a stage
 
   static __device__ __forceinline__ int swz(int r) { return (r >> 1) & 3; }
-  // row(r): address of row r (its first byte), or null for a row of zeros
+  // off(r): byte offset of row r from p, or kOutside for a row of zeros; all < bytes
   template <typename F>
-  __device__ __forceinline__ void init(int wave, int lane, F&& row) {
+  __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned bytes, int c_bytes, F&& off) {
+    base = p, span = bytes, left = c_bytes;
     c_byte = ((lane & 3) ^ swz(lane >> 2)) * 16;
 #pragma unroll
     for (int q = 0; q < LQ; ++q) {
-      const gptr p = row((q * kWaves + wave) * 16 + lane / 4);
-      inc[q] = p ? kStageC : 0;
-      ptr[q] = p ? p + c_byte : (gptr)g_zero_page;
+      const unsigned o = off((q * kWaves + wave) * 16 + lane / 4);
+      voff[q] = o == kOutside ? o : o + c_byte;
     }
   }
-  // load q of the next stage; left: bytes of c from that stage's start to the end of the row (the comparison in every
-  // stage costs little beside its 16 WI WJ matrix instructions, and a second loop without it made the compiler
-  // copy accumulators between registers from loop to loop)
-  __device__ __forceinline__ void issue(int q, lptr lds, int wave, int left) {
-    const gptr p = c_byte >= left ? (gptr)g_zero_page : ptr[q];
-    lds_load16(p, lds + (q * kWaves + wave) * 1024);
-    ptr[q] += inc[q];
+  __device__ __forceinline__ void begin_stage() { tail = c_byte >= left ? kOutside : 0; }
+  __device__ __forceinline__ Load load(int q, lptr lds, int wave) {
+    return make_load(base, span, voff[q] | tail, lds + (q * kWaves + wave) * 1024);
+  }
+  __device__ __forceinline__ void end_stage() {
+    base += kStageC;
+    left -= kStageC;
   }
   // fragment address of this lane: first row r0 (a multiple of 16)
   static __device__ __forceinline__ int lane_addr(int r0, int lane) {
@@ -117,8 +153,12 @@ struct Strided {
   static constexpr int RB = BM * 2;        // bytes per c row
   static constexpr int RPL = 1024 / RB;    // c rows per wave-wide load
   static constexpr int CPR = RB / 16;      // chunks per c row
-  gptr ptr[LQ];
-  long long inc;
+  gptr base;      // first byte of the stage to be loaded next
+  unsigned ld;    // bytes between c rows
+  int stages;     // full stages left
+  unsigned tail;  // bytes of the rows of the last, partial one
+  unsigned span;
+  unsigned voff[LQ];
 
   static __device__ __forceinline__ int swz(int c) {
     return BM >= 128 ? (c & 3) | ((c >> 3) & 1) << 2 : ((c >> 1) & 1) | ((c >> 3) & 1) << 1;
@@ -126,20 +166,24 @@ struct Strided {
   static __device__ __forceinline__ int c_row(int q, int wave, int lane) {
     return (q * kWaves + wave) * RPL + lane / CPR;
   }
-  // this lane's column of load q: `cols` exist
-  static __device__ __forceinline__ int col(int q, int wave, int lane, int cols) {
+  // this lane's byte within the row in load q: `cols` bytes exist (past them, the first ones again)
+  static __device__ __forceinline__ unsigned col(int q, int wave, int lane, unsigned cols) {
     const int slot = lane % CPR, ch = (((slot >> 1) ^ swz(c_row(q, wave, lane))) << 1) | (slot & 1);
-    return ch * 8 < cols ? ch * 8 : 0;
+    return (unsigned)ch * 16 < cols ? (unsigned)ch * 16 : 0u;
   }
-  __device__ __forceinline__ void init(int wave, int lane, gptr base, long long ld_bytes, int cols) {
-    inc = 32 * ld_bytes;
+  __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned ld_bytes, int c_rows, unsigned col_bytes) {
+    base = p, ld = ld_bytes, stages = c_rows / 32, tail = (unsigned)(c_rows % 32) * ld_bytes;
 #pragma unroll
-    for (int q = 0; q < LQ; ++q) ptr[q] = base + c_row(q, wave, lane) * ld_bytes + col(q, wave, lane, cols) * 2;
+    for (int q = 0; q < LQ; ++q) voff[q] = (unsigned)c_row(q, wave, lane) * ld + col(q, wave, lane, col_bytes);
   }
-  __device__ __forceinline__ void issue(int q, lptr lds, int wave, int lane, int left_rows) {
-    const gptr p = c_row(q, wave, lane) >= left_rows ? (gptr)g_zero_page : ptr[q];
-    lds_load16(p, lds + (q * kWaves + wave) * 1024);
-    ptr[q] += inc;
+  // the rows that exist of the next 32: the others lie past the end
+  __device__ __forceinline__ void begin_stage() { span = stages > 0 ? ld * 32 : stages == 0 ? tail : 0; }
+  __device__ __forceinline__ Load load(int q, lptr lds, int wave) {
+    return make_load(base, span, voff[q], lds + (q * kWaves + wave) * 1024);
+  }
+  __device__ __forceinline__ void end_stage() {
+    base += (size_t)ld * 32;
+    --stages;
   }
   // lane i of each 16 reads c row 8 (lane / 16) + i / 4, four columns from 4 (i % 4); the second read takes the c
   // rows 4 below.  m: index of the 16-column fragment.
@@ -178,8 +222,8 @@ struct TileKernel {
   typedef typename std::conditional<SB, Strided<BJ>, Contig<BJ, EB>>::type OpB;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
   static constexpr size_t LDS = (size_t)kDepth * STAGE;
-  static constexpr bool IDX = GATHER && OP == kOpDw;  // x rows of c through perm_src: one more load per stage
-  static constexpr int VPS = OpA::LQ + OpB::LQ + (IDX ? 1 : 0);  // vector-memory operations per stage and wave
+  static constexpr bool IDX = GATHER && OP == kOpDw;  // x rows of c through perm_src
+  static constexpr int RPL = IDX ? 1024 / (BJ * 2) : 1;  // c rows per load of B
 
   // One tile with NI row fragments per wave.
   template <int NI>
@@ -193,59 +237,74 @@ struct TileKernel {
     OpA A;
     OpB B;
     const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
+    const unsigned ldx = (unsigned)a.ldx * EB, ldw = (unsigned)a.ldw * EB, ldy = (unsigned)a.ldy * EB;
     if constexpr (OP == kOpY) {
-      A.init(wave, lane, [&](int r) -> gptr {
-        const int p = t.p0 + min(r, t.ni - 1);
-        const int xr = x_row(a, p);
-        return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
-      });
-      B.init(wave, lane, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
+      const unsigned cb = (unsigned)a.K * EB;
+      if (a.perm_src)
+        A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb, [&](int r) -> unsigned {
+          const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
+          return xr >= 0 ? (unsigned)xr * ldx : kOutside;
+        });
+      else
+        A.init(wave, lane, x + (size_t)t.p0 * a.ldx * EB, (unsigned)(t.ni - 1) * ldx + cb, cb,
+               [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
+      B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1) * ldw + cb, cb,
+             [&](int r) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
     } else if constexpr (OP == kOpDx) {
-      A.init(wave, lane, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
-      B.init(wave, lane, w + (size_t)t.j0 * EB, a.ldw * EB, t.nj);
+      const unsigned cb = (unsigned)a.N * EB;
+      A.init(wave, lane, y + (size_t)t.p0 * a.ldy * EB, (unsigned)(t.ni - 1) * ldy + cb, cb,
+             [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
+      B.init(wave, lane, w + (size_t)t.j0 * EB, ldw, t.nc, t.nj * EB);
     } else {
-      A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.ni);
-      if constexpr (!IDX) B.init(wave, lane, x + ((size_t)t.p0 * a.ldx + t.j0) * EB, a.ldx * EB, t.nj);
+      A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, ldy, t.nc, t.ni * EB);
+      if constexpr (!IDX) B.init(wave, lane, x + ((size_t)t.p0 * a.ldx + t.j0) * EB, ldx, t.nc, t.nj * EB);
     }
-    // IDX: lane l holds the x row of c row 32 s + l % 32 of the next stage s to be loaded (-1: zeros)
-    int idx = -1, idx_next = -1;
-    int bcol[OpB::LQ];
+    // IDX: perm_src of this wave's c rows of a stage, by scalar loads one stage ahead, and the offsets of the x rows
+    // they name for the stage to be loaded next (kOutside: zeros)
+    constexpr int NX = IDX ? OpB::LQ * RPL : 1;
+    int idx_next[NX];
+    unsigned idx[NX], bcol[OpB::LQ];
     auto idx_load = [&](int s) {
-      const int c = s * 32 + (lane & 31);
-      return c < t.nc ? a.perm_src[t.p0 + c] : -1;
-    };
-    auto idx_row = [&](int v) {
-      const int r = div_k(v, a.k, magic);
-      return v >= 0 && r < a.x_rows ? r : -1;
-    };
-    auto issue_b_gather = [&](int q, lptr l) {
       if constexpr (IDX) {
-        int r = __builtin_amdgcn_readlane(idx, (q * kWaves + wave) * OpB::RPL);
+        const __attribute__((address_space(4))) int* p = (const __attribute__((address_space(4))) int*)a.perm_src + t.p0;
 #pragma unroll
-        for (int i = 1; i < OpB::RPL; ++i) {
-          const int ri = __builtin_amdgcn_readlane(idx, (q * kWaves + wave) * OpB::RPL + i);
-          r = lane / OpB::CPR == i ? ri : r;
-        }
-        const gptr p = x + ((size_t)(unsigned)max(r, 0) * a.ldx + t.j0 + bcol[q]) * EB;
-        lds_load16(r >= 0 ? p : (gptr)g_zero_page, l + (q * kWaves + wave) * 1024);
+        for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * 32 + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
       }
+    };
+    auto idx_rows = [&](int s) {
+#pragma unroll
+      for (int n = 0; n < NX; ++n) {
+        const int v = idx_next[n], r = div_k(v, a.k, magic);
+        const bool ok = v >= 0 && r < a.x_rows && s * 32 + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
+        idx[n] = ok ? (unsigned)r * ldx : kOutside;
+      }
+    };
+    auto load_b_gather = [&](auto qc, lptr l) -> Load {
+      constexpr int q = qc;
+      unsigned o = idx[(q * RPL) % NX];
+      static_for<RPL - 1>([&](auto ic) { o = lane / (64 / RPL) == ic + 1 ? idx[(q * RPL + ic + 1) % NX] : o; });
+      return make_load(x + (size_t)t.j0 * EB, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + (unsigned)t.nj * EB : 0,
+                       o + bcol[q], l + (q * kWaves + wave) * 1024);
     };
     if constexpr (IDX) {
 #pragma unroll
-      for (int q = 0; q < OpB::LQ; ++q) bcol[q] = OpB::col(q, wave, lane, t.nj);
+      for (int q = 0; q < OpB::LQ; ++q) bcol[q] = OpB::col(q, wave, lane, t.nj * EB);
     }
-    // load L of stage s into its buffer
-    auto issue = [&](int L, int s, int buf) {
+    // the loads of the stage to be loaded next, into buffer buf: begin, load L = 0 .. NL-1, end
+    auto begin_stage = [&] {
+      A.begin_stage();
+      if constexpr (!IDX) B.begin_stage();
+    };
+    auto load = [&](auto Lc, int buf) -> Load {
+      constexpr int L = Lc;
       const lptr la = lds + buf * STAGE, lb = la + OpA::BYTES;
-      const int left = t.nc - s * KE;
-      if (L < OpA::LQ) {
-        if constexpr (SA) A.issue(L, la, wave, lane, left);
-        else A.issue(L, la, wave, left * EB);
-      } else {
-        if constexpr (IDX) issue_b_gather(L - OpA::LQ, lb);
-        else if constexpr (SB) B.issue(L - OpA::LQ, lb, wave, lane, left);
-        else B.issue(L - OpA::LQ, lb, wave, left * EB);
-      }
+      if constexpr (L < OpA::LQ) return A.load(L, la, wave);
+      else if constexpr (IDX) return load_b_gather(std::integral_constant<int, L - OpA::LQ>{}, lb);
+      else return B.load(L - OpA::LQ, lb, wave);
+    };
+    auto end_stage = [&] {
+      A.end_stage();
+      if constexpr (!IDX) B.end_stage();
     };
     constexpr int NL = OpA::LQ + OpB::LQ;
 
@@ -277,13 +336,17 @@ struct TileKernel {
     {
 #pragma unroll
       for (int s = 0; s < kDepth; ++s) {
-        if constexpr (IDX) idx = idx_row(idx_load(s));
-#pragma unroll
-        for (int L = 0; L < NL; ++L) issue(L, s, s);
+        if constexpr (IDX) {
+          idx_load(s);
+          idx_rows(s);
+        }
+        begin_stage();
+        static_for<NL>([&](auto Lc) { load_now(load(Lc, s)); });
+        end_stage();
       }
-      if constexpr (IDX) idx_next = idx_load(kDepth);
+      idx_load(kDepth);
       Frag fa[2][NI], fb[2][WJ];
-      MOE_WAIT_VMCNT((kDepth - 1) * NL);  // (with IDX more are outstanding: the wait is stricter than needed)
+      wait_loads<(kDepth - 1) * NL>();
       barrier_keep_loads();
 #pragma unroll
       for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0);
@@ -294,28 +357,32 @@ struct TileKernel {
       // it) and frees the buffer of stage s (its fragments are in registers), which stage s+4 then fills
       auto stage = [&](auto parity, int s) {
         constexpr int cur = decltype(parity)::value, nxt = cur ^ 1;
-        MOE_WAIT_VMCNT((kDepth - 2) * VPS);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        wait_loads<(kDepth - 2) * NL>();
         barrier_keep_loads();
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (IDX) {
-          idx = idx_row(idx_next);
-          idx_next = idx_load(s + kDepth + 1);
-          __builtin_amdgcn_sched_barrier(0);
+          idx_rows(s + kDepth);
+          idx_load(s + kDepth + 1);
         }
         const int rbuf = (s + 1) & (kDepth - 1), lbuf = s & (kDepth - 1);
         constexpr int R = WJ * NI, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
         static_for<R>([&](auto rc) {
           constexpr int r = rc, j = r / NI, i = r % NI;
-          tile_mfma(acc[j][i], fb[cur][j], fa[cur][i]);
+          constexpr int l0 = spread_lo(r, NL, R), l1 = spread_hi(r, NL, R);
+          if constexpr (l0 == 0 && l1 > 0) begin_stage();
+          if constexpr (l1 > l0) tile_mfma(acc[j][i], fb[cur][j], fa[cur][i], load(std::integral_constant<int, l0 % NL>{}, lbuf));
+          else tile_mfma(acc[j][i], fb[cur][j], fa[cur][i]);
+          static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) {
+            load_now(load(std::integral_constant<int, l0 + 1 + Lc>{}, lbuf));
+          });
+          if constexpr (l0 < NL && l1 == NL) end_stage();
           constexpr int lo = spread_lo(r, NR, T), hi = r < T ? spread_hi(r, NR, T) : lo;
           static_for<hi - lo>([&](auto mc) {
             constexpr int m = lo + mc;
             if constexpr (m < NI) fa[nxt][m] = read_a(m, rbuf);
             else fb[nxt][m - NI] = read_b(m - NI, rbuf);
           });
-          constexpr int l0 = spread_lo(r, NL, R), l1 = spread_hi(r, NL, R);
-          static_for<l1 - l0>([&](auto Lc) { issue(l0 + Lc, s + kDepth, lbuf); });
           __builtin_amdgcn_sched_barrier(0);
         });
       };
@@ -326,7 +393,7 @@ struct TileKernel {
         stage(std::integral_constant<int, 1>{}, s + 1);
         s += 2;
       } while (s < ns);
-      __builtin_amdgcn_s_waitcnt(0);  // nothing may land in LDS once the workgroup is gone
+      wait_loads<0>();  // nothing may land in LDS once the workgroup is gone
     }
 
     // ---- results.  The accumulators pass an empty asm after the wait states, so that no read of them can be
