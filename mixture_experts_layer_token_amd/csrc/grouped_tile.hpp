@@ -7,11 +7,14 @@
 //
 // A workgroup of 4 waves (2 x 2) computes up to 32 WI x 32 WJ results of one expert; a wave owns 16 WI x 16 WJ of
 // them.  Bound by the matrix cores for many rows per expert, by the weights' bytes for few.
-//  - 4 stages of 64 bytes of c per row (32 bf16 or 64 int8) wait in LDS or on their way there, written by direct
-//    global->LDS loads of 16 bytes per lane; the fragments of the stage after the current one are read into
-//    registers while the current one is multiplied, so each buffer is free again one stage early and loads
-//    have three stages of time to land.  One barrier per stage; it leaves loads in flight.
-//  - an operand contiguous along c sits in LDS as rows of 64 bytes and is read as MFMA fragments directly
+//  - two stages of 128 bytes of c per row (64 bf16 or 128 int8, two MFMA steps) in LDS, written by direct
+//    global->LDS loads of 16 bytes per lane.  The fragments of the next step are read into registers while the
+//    current one is multiplied; a stage's buffer is therefore free when its second step begins, the loads of
+//    the stage after next are issued then and have a step and a half to land.  One barrier per stage.
+//  - whole 128-byte lines: with stages of half a line (four of 64 bytes in the same LDS) every line came from L2
+//    twice, as the second half was asked for when the L1 had long dropped it -- 16.9 GB of operands as 30 GB of
+//    L2 hits on the Mixtral-shaped gate/up product, the whole of an L1's fill rate.
+//  - an operand contiguous along c sits in LDS as rows of 128 bytes and is read as MFMA fragments directly
 //    (ds_read_b128); one that is strided along c sits there as it is in memory, c rows of up to 512 bytes, and is
 //    transposed on the way to the registers by ds_read_b64_tr_b16 (16 lanes read 4 rows of 16 elements,
 //    lane i receives column i), so neither needs a transposed copy in memory.  16-byte chunks (32-byte
@@ -65,8 +68,8 @@ __device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x
 }
 
 typedef __attribute__((address_space(3))) char* lptr;
-constexpr int kDepth = 4;     // stages
-constexpr int kStageC = 64;   // bytes of c per row and stage
+constexpr int kStageC = 128;  // bytes of c per row and stage
+constexpr int kStageRows = kStageC / 2;  // c rows of a stage, bf16
 constexpr int kWaves = 4;
 
 // ------------------------------------------------------------------ operands
@@ -106,7 +109,7 @@ __device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x
 // of 16 rows are read.
 template <int BM, int EB>
 struct Contig {
-  static constexpr int LQ = BM / 64;
+  static constexpr int LQ = BM / 32;
   static constexpr int BYTES = BM * kStageC;
   gptr base;          // first byte of the stage to be loaded next, row 0
   unsigned span;      // bytes of the operand; the lanes that are not kOutside never pass its end
@@ -115,15 +118,14 @@ struct Contig {
   unsigned tail;      // its part of the next stage lies past the end of c: kOutside, else 0
   int c_byte;         // its byte of c within a stage
 
-  static __device__ __forceinline__ int swz(int r) { return (r >> 1) & 3; }
   // off(r): byte offset of row r from p, or kOutside for a row of zeros; all < bytes
   template <typename F>
   __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned bytes, int c_bytes, F&& off) {
     base = p, span = bytes, left = c_bytes;
-    c_byte = ((lane & 3) ^ swz(lane >> 2)) * 16;
+    c_byte = ((lane & 7) ^ (lane >> 3)) * 16;  // 8 rows per load: chunk c of row r goes to slot c ^ (r & 7)
 #pragma unroll
     for (int q = 0; q < LQ; ++q) {
-      const unsigned o = off((q * kWaves + wave) * 16 + lane / 4);
+      const unsigned o = off((q * kWaves + wave) * 8 + lane / 8);
       voff[q] = o == kOutside ? o : o + c_byte;
     }
   }
@@ -135,20 +137,21 @@ struct Contig {
     base += kStageC;
     left -= kStageC;
   }
-  // fragment address of this lane: first row r0 (a multiple of 16)
+  // fragment address of this lane, step 0: first row r0 (a multiple of 16)
   static __device__ __forceinline__ int lane_addr(int r0, int lane) {
-    return (r0 + (lane & 15)) * kStageC + ((lane >> 4) ^ swz(lane & 15)) * 16;
+    return (r0 + (lane & 15)) * kStageC + ((lane >> 4) ^ (lane & 7)) * 16;
   }
+  // rows 16 f from there, MFMA step h of the stage
   template <typename Frag>
-  static __device__ __forceinline__ Frag read(lptr base, int addr, int f, int step16) {
-    return *(const __attribute__((address_space(3))) Frag*)(base + addr + f * step16 * 16 * kStageC);
+  static __device__ __forceinline__ Frag read(lptr base, int addr, int f, int h) {
+    return *(const __attribute__((address_space(3))) Frag*)(base + (addr ^ (h * 64)) + f * 16 * kStageC);
   }
 };
 
 // (bf16 only) BM columns of memory rows that are c; swizzled in 32-byte pairs of chunks
 template <int BM>
 struct Strided {
-  static constexpr int LQ = BM / 64;
+  static constexpr int LQ = BM / 32;
   static constexpr int BYTES = BM * kStageC;
   static constexpr int RB = BM * 2;        // bytes per c row
   static constexpr int RPL = 1024 / RB;    // c rows per wave-wide load
@@ -172,17 +175,17 @@ struct Strided {
     return (unsigned)ch * 16 < cols ? (unsigned)ch * 16 : 0u;
   }
   __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned ld_bytes, int c_rows, unsigned col_bytes) {
-    base = p, ld = ld_bytes, stages = c_rows / 32, tail = (unsigned)(c_rows % 32) * ld_bytes;
+    base = p, ld = ld_bytes, stages = c_rows / kStageRows, tail = (unsigned)(c_rows % kStageRows) * ld_bytes;
 #pragma unroll
     for (int q = 0; q < LQ; ++q) voff[q] = (unsigned)c_row(q, wave, lane) * ld + col(q, wave, lane, col_bytes);
   }
-  // the rows that exist of the next 32: the others lie past the end
-  __device__ __forceinline__ void begin_stage() { span = stages > 0 ? ld * 32 : stages == 0 ? tail : 0; }
+  // the rows that exist of the next stage: the others lie past the end
+  __device__ __forceinline__ void begin_stage() { span = stages > 0 ? ld * kStageRows : stages == 0 ? tail : 0; }
   __device__ __forceinline__ Load load(int q, lptr lds, int wave) {
     return make_load(base, span, voff[q], lds + (q * kWaves + wave) * 1024);
   }
   __device__ __forceinline__ void end_stage() {
-    base += (size_t)ld * 32;
+    base += (size_t)ld * kStageRows;
     --stages;
   }
   // lane i of each 16 reads c row 8 (lane / 16) + i / 4, four columns from 4 (i % 4); the second read takes the c
@@ -191,10 +194,10 @@ struct Strided {
     const int c = 8 * (lane >> 4) + ((lane & 15) >> 2);
     return c * RB + ((m ^ swz(c)) << 5) + 8 * (lane & 3);
   }
-  // fragment m ^ x (x: the bits by which it differs from lane_addr's)
-  static __device__ __forceinline__ bf16x8 read(lptr base, int addr, int x) {
+  // fragment m ^ x (x: the bits by which it differs from lane_addr's), MFMA step h of the stage
+  static __device__ __forceinline__ bf16x8 read(lptr base, int addr, int x, int h) {
     typedef __attribute__((address_space(3))) s16x4* p4;
-    const lptr p = base + (addr ^ (x << 5));
+    const lptr p = base + (addr ^ (x << 5)) + h * 32 * RB;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)p);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * RB));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -221,7 +224,7 @@ struct TileKernel {
   typedef typename std::conditional<SA, Strided<BI>, Contig<BI, EB>>::type OpA;
   typedef typename std::conditional<SB, Strided<BJ>, Contig<BJ, EB>>::type OpB;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
-  static constexpr size_t LDS = (size_t)kDepth * STAGE;
+  static constexpr size_t LDS = (size_t)2 * STAGE;
   static constexpr bool IDX = GATHER && OP == kOpDw;  // x rows of c through perm_src
   static constexpr int RPL = IDX ? 1024 / (BJ * 2) : 1;  // c rows per load of B
 
@@ -268,14 +271,14 @@ struct TileKernel {
       if constexpr (IDX) {
         const __attribute__((address_space(4))) int* p = (const __attribute__((address_space(4))) int*)a.perm_src + t.p0;
 #pragma unroll
-        for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * 32 + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
+        for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * kStageRows + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
       }
     };
     auto idx_rows = [&](int s) {
 #pragma unroll
       for (int n = 0; n < NX; ++n) {
         const int v = idx_next[n], r = div_k(v, a.k, magic);
-        const bool ok = v >= 0 && r < a.x_rows && s * 32 + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
+        const bool ok = v >= 0 && r < a.x_rows && s * kStageRows + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
         idx[n] = ok ? (unsigned)r * ldx : kOutside;
       }
     };
@@ -314,15 +317,15 @@ struct TileKernel {
     else addr_a = OpA::lane_addr(16 * wi, lane);
     if constexpr (SB) addr_b = OpB::lane_addr(WJ * wj, lane);
     else addr_b = OpB::lane_addr(16 * WJ * wj, lane);
-    auto read_a = [&](int f, int buf) -> Frag {
+    auto read_a = [&](int f, int buf, int h) -> Frag {
       const lptr l = lds + buf * STAGE;
-      if constexpr (SA) return OpA::read(l, addr_a, 2 * f);
-      else return OpA::template read<Frag>(l, addr_a, f, 2);
+      if constexpr (SA) return OpA::read(l, addr_a, 2 * f, h);
+      else return OpA::template read<Frag>(l, addr_a, 2 * f, h);
     };
-    auto read_b = [&](int f, int buf) -> Frag {
+    auto read_b = [&](int f, int buf, int h) -> Frag {
       const lptr l = lds + buf * STAGE + OpA::BYTES;
-      if constexpr (SB) return OpB::read(l, addr_b, f);
-      else return OpB::template read<Frag>(l, addr_b, f, 1);
+      if constexpr (SB) return OpB::read(l, addr_b, f, h);
+      else return OpB::template read<Frag>(l, addr_b, f, h);
     };
 
     Acc acc[WJ][NI];
@@ -331,11 +334,11 @@ struct TileKernel {
 #pragma unroll
       for (int i = 0; i < NI; ++i) acc[j][i] = Acc{};
 
-    // ---- prologue: the first kDepth stages
+    // ---- prologue: the first two stages, the fragments of step 0
     const int ns = (t.nc + KE - 1) / KE;  // >= 1
     {
 #pragma unroll
-      for (int s = 0; s < kDepth; ++s) {
+      for (int s = 0; s < 2; ++s) {
         if constexpr (IDX) {
           idx_load(s);
           idx_rows(s);
@@ -344,55 +347,58 @@ struct TileKernel {
         static_for<NL>([&](auto Lc) { load_now(load(Lc, s)); });
         end_stage();
       }
-      idx_load(kDepth);
+      idx_load(2);
       Frag fa[2][NI], fb[2][WJ];
-      wait_loads<(kDepth - 1) * NL>();
+      wait_loads<NL>();
       barrier_keep_loads();
 #pragma unroll
-      for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0);
+      for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0, 0);
 #pragma unroll
-      for (int j = 0; j < WJ; ++j) fb[0][j] = read_b(j, 0);
+      for (int j = 0; j < WJ; ++j) fb[0][j] = read_b(j, 0, 0);
 
-      // ---- one stage: at its start the barrier publishes stage s+1 (every wave has waited for its own loads of
-      // it) and frees the buffer of stage s (its fragments are in registers), which stage s+4 then fills
-      auto stage = [&](auto parity, int s) {
-        constexpr int cur = decltype(parity)::value, nxt = cur ^ 1;
+      // ---- one MFMA step: step h of stage s is multiplied, the next one's fragments are read.  With h = 1 the
+      // barrier comes first: it publishes stage s+1 (every wave has waited for its own loads of it) and frees the
+      // buffer of stage s (its last fragments are in registers), into which stage s+2 is then loaded.
+      auto step = [&](auto hc, int s) {
+        constexpr int h = hc;
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        wait_loads<(kDepth - 2) * NL>();
-        barrier_keep_loads();
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (IDX) {
-          idx_rows(s + kDepth);
-          idx_load(s + kDepth + 1);
+        if constexpr (h == 1) {
+          wait_loads<0>();
+          barrier_keep_loads();
+          if constexpr (IDX) {
+            idx_rows(s + 2);
+            idx_load(s + 3);
+          }
         }
-        const int rbuf = (s + 1) & (kDepth - 1), lbuf = s & (kDepth - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const int cbuf = s & 1, rbuf = h == 0 ? cbuf : cbuf ^ 1;
+        // slots: reads over the first three quarters of the MFMAs, loads over the first half
         constexpr int R = WJ * NI, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
+        constexpr int NQ = h == 1 ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
         static_for<R>([&](auto rc) {
           constexpr int r = rc, j = r / NI, i = r % NI;
-          constexpr int l0 = spread_lo(r, NL, R), l1 = spread_hi(r, NL, R);
+          constexpr int l0 = spread_lo(r, NQ, TL), l1 = r < TL ? spread_hi(r, NQ, TL) : l0;
           if constexpr (l0 == 0 && l1 > 0) begin_stage();
-          if constexpr (l1 > l0) tile_mfma(acc[j][i], fb[cur][j], fa[cur][i], load(std::integral_constant<int, l0 % NL>{}, lbuf));
-          else tile_mfma(acc[j][i], fb[cur][j], fa[cur][i]);
+          if constexpr (l1 > l0) tile_mfma(acc[j][i], fb[h][j], fa[h][i], load(std::integral_constant<int, l0>{}, cbuf));
+          else tile_mfma(acc[j][i], fb[h][j], fa[h][i]);
           static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) {
-            load_now(load(std::integral_constant<int, l0 + 1 + Lc>{}, lbuf));
+            load_now(load(std::integral_constant<int, l0 + 1 + Lc>{}, cbuf));
           });
-          if constexpr (l0 < NL && l1 == NL) end_stage();
+          if constexpr (l1 > l0 && l1 == NQ) end_stage();
           constexpr int lo = spread_lo(r, NR, T), hi = r < T ? spread_hi(r, NR, T) : lo;
           static_for<hi - lo>([&](auto mc) {
             constexpr int m = lo + mc;
-            if constexpr (m < NI) fa[nxt][m] = read_a(m, rbuf);
-            else fb[nxt][m - NI] = read_b(m - NI, rbuf);
+            if constexpr (m < NI) fa[h ^ 1][m] = read_a(m, rbuf, h ^ 1);
+            else fb[h ^ 1][m - NI] = read_b(m - NI, rbuf, h ^ 1);
           });
           __builtin_amdgcn_sched_barrier(0);
         });
       };
-      // (an odd number of stages ends with one over zeros)
       int s = 0;
       do {
-        stage(std::integral_constant<int, 0>{}, s);
-        stage(std::integral_constant<int, 1>{}, s + 1);
-        s += 2;
-      } while (s < ns);
+        step(std::integral_constant<int, 0>{}, s);
+        step(std::integral_constant<int, 1>{}, s);
+      } while (++s < ns);
       wait_loads<0>();  // nothing may land in LDS once the workgroup is gone
     }
 
