@@ -204,6 +204,27 @@ struct Strided {
   }
 };
 
+// ------------------------------------------------------------------ results
+// two fp32 to bf16, nearest-even (one instruction)
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 b2;
+  return __builtin_bit_cast(unsigned, b2{(__bf16)lo, (__bf16)hi});
+}
+
+// 16 rows of w columns from a wave's LDS region, of which ni rows and nj columns exist; they start at row i0, column
+// j0 of the tile.  Element by element: the rare layouts take it.
+__device__ __forceinline__ void store_rows(const float* reg, char* out, long long ldc, int ni, int nj, int i0,
+                                                     int j0, int w, const float* sw, int bf16) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (int r = 0; r < min(ni, 16); ++r)
+#pragma unroll 1
+    for (int c = lane; c < min(nj, w); c += 64) {
+      const float v = reg[r * w + c];
+      store_out(out, (size_t)(i0 + r) * ldc + j0 + c, sw ? v * sw[j0 + c] : v, bf16);
+    }
+}
+
 // ------------------------------------------------------------------ tiles
 struct TileItem {
   int e, i0, ni, j0, nj, p0, nc;  // expert; first i and j and how many exist; first grouped row; length of c
@@ -409,53 +430,74 @@ struct TileKernel {
     for (int j = 0; j < WJ; ++j)
 #pragma unroll
       for (int i = 0; i < NI; ++i) asm volatile("" : "+a"(acc[j][i]));
-    const int q4 = (lane >> 4) * 4;
+    // A lane's four results are neighbouring columns of one row: 8 or 16 bytes per store, straight from the
+    // accumulators.  The code is kept short on purpose: it runs once per tile, so it comes from L2, and with
+    // every address and rounding spelled out it took 28 us per tile.
+    const int rlane = wi * 16 + (lane & 15);  // row of fragment 0; the others follow 32 rows apart
+    const int clane = WJ * wj * 16 + (lane >> 4) * 4;  // column of fragment 0; the others follow 16 apart
     const long long ldc = OP == kOpY ? a.ldy : OP == kOpDx ? a.ldx : a.ldw;
     const int ob = a.out_bf16 ? 2 : 4;
     char* out = (char*)(OP == kOpY ? a.y : OP == kOpDx ? a.x : a.w);
-    out += (OP == kOpDw ? (size_t)t.e * a.w_stride + (size_t)t.i0 * ldc : (size_t)t.p0 * ldc) * ob;
-    const bool wide = ((size_t)out | (size_t)(ldc * ob)) % (4 * ob) == 0;  // rows start on a store's width
-    const int rlane = wi * 16 + (lane & 15);  // row of fragment 0; the others follow 32 rows apart
-    float rs[NI];
-    if constexpr (TYPE == kI8) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
+    out += ((OP == kOpDw ? (size_t)t.e * a.w_stride + (size_t)t.i0 * ldc : (size_t)t.p0 * ldc) + t.j0) * ob;
+    const float* sw = TYPE == kI8 ? a.w_scale + (size_t)t.e * a.N + t.j0 : nullptr;
+    auto row_scale = [&](int i) {
+      if constexpr (TYPE == kI8) {
         const int xr = x_row(a, t.p0 + min(32 * i + rlane, t.ni - 1));
-        rs[i] = xr >= 0 ? a.x_scale[xr] : 0.f;
+        return xr >= 0 ? a.x_scale[xr] : 0.f;
       }
-    }
-#pragma unroll
-    for (int j = 0; j < WJ; ++j) {
-      const int jj = (WJ * wj + j) * 16 + q4, left = t.nj - jj;
-      if (left <= 0) continue;
-      const size_t col = (size_t)t.j0 + jj;
-      float sw[4];
+      return 1.f;
+    };
+    // rows that start on a store's width and end on four columns
+    if (((size_t)out | (size_t)(ldc * ob)) % (4 * ob) == 0 && t.nj % 4 == 0) {
+      f32x4 cs[TYPE == kI8 ? WJ : 1];
       if constexpr (TYPE == kI8) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sw[r] = a.w_scale[(size_t)t.e * a.N + t.j0 + min(jj + r, t.nj - 1)];
+        for (int j = 0; j < WJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) cs[j][r] = sw[min(clane + 16 * j + r, t.nj - 1)];
       }
+      auto rows = [&](auto bf) {
+        constexpr bool BF = decltype(bf)::value;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          float rs = 1.f;
+          if constexpr (TYPE == kI8) rs = row_scale(i);
+          if (32 * i + rlane >= t.ni) continue;
+          char* p = out + ((size_t)(32 * i + rlane) * ldc + clane) * (BF ? 2 : 4);
+#pragma unroll
+          for (int j = 0; j < WJ; ++j) {
+            if (clane + 16 * j >= t.nj) continue;
+            f32x4 v;
+            if constexpr (TYPE == kI8) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = (float)acc[j][i][r] * rs * cs[j][r];
+            } else {
+              v = acc[j][i];
+            }
+            if constexpr (BF) *(u32x2*)(p + 32 * j) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            else *(f32x4*)(p + 64 * j) = v;
+          }
+        }
+      };
+      if (a.out_bf16) rows(std::true_type{});
+      else rows(std::false_type{});
+    } else {
+      // any other: 16 rows at a time through LDS (a region per wave; no wave reads operands any more), element by
+      // element
+      barrier_keep_loads();
+      float* reg = (float*)(lds + wave * (16 * 16 * WJ * 4));
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int ii = 32 * i + rlane;
-        if (ii >= t.ni) continue;
-        char* row = out + (size_t)ii * ldc * ob;
-        f32x4 v;
+        const float rs = row_scale(i);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (TYPE == kI8) v[r] = (float)acc[j][i][r] * rs[i] * sw[r];
-          else v[r] = acc[j][i][r];
-        }
-        if (wide && left >= 4) {
-          if (a.out_bf16)
-            *(u32x2*)(row + col * 2) = u32x2{(unsigned)f32_to_bf16_rne(v[0]) | ((unsigned)f32_to_bf16_rne(v[1]) << 16),
-                                             (unsigned)f32_to_bf16_rne(v[2]) | ((unsigned)f32_to_bf16_rne(v[3]) << 16)};
-          else
-            *(f32x4*)(row + col * 4) = v;
-        } else {
+        for (int j = 0; j < WJ; ++j) {
+          f32x4 v;
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (r < left) store_out(row, col + r, v[r], a.out_bf16);
+          for (int r = 0; r < 4; ++r) v[r] = TYPE == kI8 ? (float)acc[j][i][r] * rs : (float)acc[j][i][r];
+          *(f32x4*)(reg + (lane & 15) * 16 * WJ + 16 * j + (lane >> 4) * 4) = v;
         }
+        store_rows(reg, out, ldc, t.ni - (32 * i + wi * 16), t.nj - WJ * wj * 16, 32 * i + wi * 16, WJ * wj * 16, 16 * WJ, sw,
+                   a.out_bf16);
       }
     }
   }
