@@ -21,6 +21,9 @@ struct GroupArgs {
   const float* x_scale;  // 8-bit operands: scale of every x row and of every w row ([E][N])
   const float* w_scale;
   int out_bf16;
+  // weights' gradient: parts each group's rows are cut into; with more than one, w is fp32 partial sums
+  // [split][E][N][K]
+  int split;
 };
 
 // Rows of expert e, clamped so that no offsets, however wrong, lead outside [0, rows).
@@ -106,10 +109,15 @@ inline bool tile_spans_fit(const GroupArgs& a, int op, int eb) {
   return (op == kOpDx || x) && (op == kOpDw || rows(256, a.ldw)) && (op == kOpY || rows(256, a.ldy));
 }
 
-// grouped_tile_*.hip: the MFMA tile kernel, rows and pointers on 16-byte boundaries
-int launch_tile_y(const GroupArgs& a, int type, int wi, hipStream_t s);
-int launch_tile_dx(const GroupArgs& a, int wi, hipStream_t s);
-int launch_tile_dw(const GroupArgs& a, int wi, hipStream_t s);
+// grouped_tile_*.hip: the MFMA tile kernel.  kLarge: 256 x 256 results per workgroup (bf16, int8), kSmall: 128 x 128, both
+// for rows on 16-byte boundaries and spans that fit; kStaged: 128 x 128 for any others.
+enum TileShape { kLarge, kSmall, kStaged };
+int launch_tile_y_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_y_i8(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_dx_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_dw_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_dw_bf16_gather(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_f32(const GroupArgs& a, int op, TileShape t, hipStream_t s);
 // the kernel that suits the call; ws holds grouped_workspace bytes
 int launch_grouped(const GroupArgs& a, int op, int type, void* ws, hipStream_t s);
 size_t grouped_workspace(int type, int rows, int N, int K, int E);

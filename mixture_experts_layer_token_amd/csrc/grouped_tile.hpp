@@ -43,13 +43,21 @@ template <>
 struct TileT<kBf16> {
   typedef bf16x8 Frag;
   typedef f32x4 Acc;
-  static constexpr int EB = 2;
+  static constexpr int EB = 2, MPF = 1;  // bytes of an element, MFMAs per pair of fragments
 };
 template <>
 struct TileT<kI8> {
   typedef i32x4 Frag;
   typedef i32x4 Acc;
-  static constexpr int EB = 1;
+  static constexpr int EB = 1, MPF = 1;
+};
+// An fp32 fragment is 16 bytes of c per lane as well: lane group g (lane / 16) holds c = 4 g .. 4 g + 3, and MFMA e takes
+// element e of every lane, that is c = e, 4 + e, 8 + e, 12 + e.
+template <>
+struct TileT<kF32> {
+  typedef f32x4 Frag;
+  typedef f32x4 Acc;
+  static constexpr int EB = 4, MPF = 4;
 };
 
 // Waits until at most N of this wave's loads are in flight (the compiler does not know the ones in inline assembly)
@@ -60,16 +68,21 @@ __device__ __forceinline__ void wait_loads() {
 
 // In-place MFMA on an accumulator held in AGPRs; b is the first operand (see the head of the file).  Its operands
 // come straight from LDS reads, which the compiler waits for; no vector instruction writes them.
+template <int E>
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
+template <int E>
 __device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x4& a) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+template <int E>
+__device__ __forceinline__ void tile_mfma(f32x4& acc, const f32x4& b, const f32x4& a) {
+  asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+a"(acc) : "v"(b[E]), "v"(a[E]));
 }
 
 typedef __attribute__((address_space(3))) char* lptr;
 constexpr int kStageC = 128;  // bytes of c per row and stage
-constexpr int kStageRows = kStageC / 2;  // c rows of a stage, bf16
 constexpr int kWaves = 4;
 
 // ------------------------------------------------------------------ operands
@@ -96,17 +109,41 @@ __device__ __forceinline__ void load_now(const Load& d) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                : : "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
+template <int E>
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a, const Load& d) {
   asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
                : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
+template <int E>
 __device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x4& a, const Load& d) {
   asm volatile("s_mov_b32 m0, %3\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
                : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
+template <int E>
+__device__ __forceinline__ void tile_mfma(f32x4& acc, const f32x4& b, const f32x4& a, const Load& d) {
+  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x4_f32 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+               : "+a"(acc) : "v"(b[E]), "v"(a[E]), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+}
+
+// 16 bytes at any element-aligned address, of which the first n exist (the others are zeros)
+template <int EB>
+__device__ __forceinline__ u32x4 load_part(gptr p, int n) {
+  typedef u32x4 __attribute__((aligned(1))) any4;
+  typedef typename std::conditional<EB == 1, unsigned char, typename std::conditional<EB == 2, unsigned short, unsigned>::type>::type El;
+  u32x4 v = {0, 0, 0, 0};
+  if (n >= 16) {
+    v = *(const __attribute__((address_space(1))) any4*)p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16 / EB; ++i)
+      if (i * EB < n) v[i * EB / 4] |= (unsigned)((const __attribute__((address_space(1))) El*)p)[i] << (i * EB % 4 * 8);
+  }
+  return v;
+}
 
 // One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; fragments
-// of 16 rows are read.
+// of 16 rows are read.  Two forms: `load` gives a direct load to LDS (16-byte rows, spans within 32 bits), `fetch`
+// the same 16 bytes in registers by ordinary loads at any address, for `put` to write to the same place.
 template <int BM, int EB>
 struct Contig {
   static constexpr int LQ = BM / 32;
@@ -117,6 +154,7 @@ struct Contig {
   unsigned voff[LQ];  // this lane's bytes
   unsigned tail;      // its part of the next stage lies past the end of c: kOutside, else 0
   int c_byte;         // its byte of c within a stage
+  gptr row[LQ];       // (fetch) its rows; null: zeros
 
   // off(r): byte offset of row r from p, or kOutside for a row of zeros; all < bytes
   template <typename F>
@@ -128,6 +166,20 @@ struct Contig {
       const unsigned o = off((q * kWaves + wave) * 8 + lane / 8);
       voff[q] = o == kOutside ? o : o + c_byte;
     }
+  }
+  // rowp(r): address of row r, or null for a row of zeros
+  template <typename F>
+  __device__ __forceinline__ void init_fetch(int wave, int lane, int c_bytes, F&& rowp) {
+    left = c_bytes;
+    c_byte = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+    for (int q = 0; q < LQ; ++q) row[q] = rowp((q * kWaves + wave) * 8 + lane / 8);
+  }
+  __device__ __forceinline__ u32x4 fetch(int q) const { return load_part<EB>(row[q] + c_byte, row[q] ? left - c_byte : 0); }
+  __device__ __forceinline__ void end_fetch() {
+#pragma unroll
+    for (int q = 0; q < LQ; ++q) row[q] += row[q] ? kStageC : 0;
+    left -= kStageC;
   }
   __device__ __forceinline__ void begin_stage() { tail = c_byte >= left ? kOutside : 0; }
   __device__ __forceinline__ Load load(int q, lptr lds, int wave) {
@@ -148,59 +200,92 @@ struct Contig {
   }
 };
 
-// (bf16 only) BM columns of memory rows that are c; swizzled in 32-byte pairs of chunks
-template <int BM>
+// BM columns of memory rows that are c, swizzled in units of 16 columns.
+template <int BM, int EB>
 struct Strided {
   static constexpr int LQ = BM / 32;
   static constexpr int BYTES = BM * kStageC;
-  static constexpr int RB = BM * 2;        // bytes per c row
-  static constexpr int RPL = 1024 / RB;    // c rows per wave-wide load
-  static constexpr int CPR = RB / 16;      // chunks per c row
+  static constexpr int ROWS = kStageC / EB;  // c rows of a stage
+  static constexpr int RB = BM * EB;         // bytes per c row
+  static constexpr int RPL = 1024 / RB;      // c rows per wave-wide load
+  static constexpr int CPR = RB / 16;        // chunks per c row
+  static constexpr int US = EB == 2 ? 1 : 2; // log2 of the chunks of a unit
+  static_assert(EB == 2 ? BM >= 64 : BM == 128, "bank layout");
   gptr base;      // first byte of the stage to be loaded next
   unsigned ld;    // bytes between c rows
   int stages;     // full stages left
   unsigned tail;  // bytes of the rows of the last, partial one
   unsigned span;
   unsigned voff[LQ];
+  long long ld64;  // (fetch)
+  int left, ncol;  // (fetch) c rows and bytes of a row that exist
 
+  // The rows that one read touches -- bf16: c = 8 g + 0..3, fp32: c = 4 g + e, for lane groups g = 0..3 -- get
+  // different units in the same place, so that they fall into different banks.
   static __device__ __forceinline__ int swz(int c) {
+    if constexpr (EB == 4) return (c >> 2) & 3;
     return BM >= 128 ? (c & 3) | ((c >> 3) & 1) << 2 : ((c >> 1) & 1) | ((c >> 3) & 1) << 1;
   }
   static __device__ __forceinline__ int c_row(int q, int wave, int lane) {
     return (q * kWaves + wave) * RPL + lane / CPR;
   }
-  // this lane's byte within the row in load q: `cols` bytes exist (past them, the first ones again)
+  // this lane's byte within the row in load q
+  static __device__ __forceinline__ unsigned col_of(int q, int wave, int lane) {
+    const int slot = lane % CPR;
+    return (unsigned)((((slot >> US) ^ swz(c_row(q, wave, lane))) << US) | (slot & ((1 << US) - 1))) * 16;
+  }
+  // the same where `cols` bytes exist: past them, the first ones again
   static __device__ __forceinline__ unsigned col(int q, int wave, int lane, unsigned cols) {
-    const int slot = lane % CPR, ch = (((slot >> 1) ^ swz(c_row(q, wave, lane))) << 1) | (slot & 1);
-    return (unsigned)ch * 16 < cols ? (unsigned)ch * 16 : 0u;
+    const unsigned c = col_of(q, wave, lane);
+    return c < cols ? c : 0u;
   }
   __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned ld_bytes, int c_rows, unsigned col_bytes) {
-    base = p, ld = ld_bytes, stages = c_rows / kStageRows, tail = (unsigned)(c_rows % kStageRows) * ld_bytes;
+    base = p, ld = ld_bytes, stages = c_rows / ROWS, tail = (unsigned)(c_rows % ROWS) * ld_bytes;
 #pragma unroll
     for (int q = 0; q < LQ; ++q) voff[q] = (unsigned)c_row(q, wave, lane) * ld + col(q, wave, lane, col_bytes);
   }
   // the rows that exist of the next stage: the others lie past the end
-  __device__ __forceinline__ void begin_stage() { span = stages > 0 ? ld * kStageRows : stages == 0 ? tail : 0; }
+  __device__ __forceinline__ void begin_stage() { span = stages > 0 ? ld * ROWS : stages == 0 ? tail : 0; }
   __device__ __forceinline__ Load load(int q, lptr lds, int wave) {
     return make_load(base, span, voff[q], lds + (q * kWaves + wave) * 1024);
   }
   __device__ __forceinline__ void end_stage() {
-    base += (size_t)ld * kStageRows;
+    base += (size_t)ld * ROWS;
     --stages;
   }
-  // lane i of each 16 reads c row 8 (lane / 16) + i / 4, four columns from 4 (i % 4); the second read takes the c
-  // rows 4 below.  m: index of the 16-column fragment.
+  __device__ __forceinline__ void init_fetch(gptr p, long long ld_bytes, int c_rows, int col_bytes) {
+    base = p, ld64 = ld_bytes, left = c_rows, ncol = col_bytes;
+  }
+  __device__ __forceinline__ u32x4 fetch(int q, int wave, int lane) const {
+    const int c = c_row(q, wave, lane), o = (int)col_of(q, wave, lane);
+    return load_part<EB>(base + c * ld64 + o, c < left ? ncol - o : 0);
+  }
+  __device__ __forceinline__ void end_fetch() {
+    base += ld64 * ROWS;
+    left -= ROWS;
+  }
+  // bf16: lane i of each 16 reads c row 8 (lane / 16) + i / 4, four columns from 4 (i % 4); the second read takes the c
+  // rows 4 below.  fp32: lane i of group g reads column i of the c rows 4 g .. 4 g + 3.  m: index of the 16-column
+  // fragment.
   static __device__ __forceinline__ int lane_addr(int m, int lane) {
+    if constexpr (EB == 4) return 4 * (lane >> 4) * RB + ((m ^ (lane >> 4)) << 6) + 4 * (lane & 15);
     const int c = 8 * (lane >> 4) + ((lane & 15) >> 2);
     return c * RB + ((m ^ swz(c)) << 5) + 8 * (lane & 3);
   }
   // fragment m ^ x (x: the bits by which it differs from lane_addr's), MFMA step h of the stage
-  static __device__ __forceinline__ bf16x8 read(lptr base, int addr, int x, int h) {
-    typedef __attribute__((address_space(3))) s16x4* p4;
-    const lptr p = base + (addr ^ (x << 5)) + h * 32 * RB;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * RB));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  template <typename Frag>
+  static __device__ __forceinline__ Frag read(lptr base, int addr, int x, int h) {
+    if constexpr (EB == 4) {
+      const __attribute__((address_space(3))) float* p =
+          (const __attribute__((address_space(3))) float*)(base + (addr ^ (x << 6)) + h * 16 * RB);
+      return Frag{p[0], p[RB / 4], p[2 * RB / 4], p[3 * RB / 4]};
+    } else {
+      typedef __attribute__((address_space(3))) s16x4* p4;
+      const lptr p = base + (addr ^ (x << 5)) + h * 32 * RB;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * RB));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
   }
 };
 
@@ -234,7 +319,8 @@ struct TileItem {
 // off by less than 1 / k there.
 __device__ __forceinline__ int div_k(int s, int k, unsigned magic) { return k == 1 ? s : (int)__umulhi((unsigned)s, magic); }
 
-template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+// STAGED: operands pass through registers (any alignment, stride and extent)
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
 struct TileKernel {
   typedef TileT<TYPE> TT;
   typedef typename TT::Frag Frag;
@@ -242,12 +328,12 @@ struct TileKernel {
   static constexpr int EB = TT::EB, KE = kStageC / EB;  // elements of c per stage
   static constexpr int BI = 32 * WI, BJ = 32 * WJ;
   static constexpr bool SA = OP == kOpDw, SB = OP != kOpY;  // strided operands
-  typedef typename std::conditional<SA, Strided<BI>, Contig<BI, EB>>::type OpA;
-  typedef typename std::conditional<SB, Strided<BJ>, Contig<BJ, EB>>::type OpB;
+  typedef typename std::conditional<SA, Strided<BI, EB>, Contig<BI, EB>>::type OpA;
+  typedef typename std::conditional<SB, Strided<BJ, EB>, Contig<BJ, EB>>::type OpB;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
   static constexpr size_t LDS = (size_t)2 * STAGE;
-  static constexpr bool IDX = GATHER && OP == kOpDw;  // x rows of c through perm_src
-  static constexpr int RPL = IDX ? 1024 / (BJ * 2) : 1;  // c rows per load of B
+  static constexpr bool IDX = GATHER && OP == kOpDw && !STAGED;  // x rows of c through perm_src
+  static constexpr int RPL = IDX ? 1024 / (BJ * EB) : 1;  // c rows per load of B
 
   // One tile with NI row fragments per wave.
   template <int NI>
@@ -262,7 +348,21 @@ struct TileKernel {
     OpB B;
     const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
     const unsigned ldx = (unsigned)a.ldx * EB, ldw = (unsigned)a.ldw * EB, ldy = (unsigned)a.ldy * EB;
-    if constexpr (OP == kOpY) {
+    if constexpr (STAGED) {
+      if constexpr (OP == kOpY) {
+        A.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr {
+          const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
+          return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
+        });
+        B.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
+      } else if constexpr (OP == kOpDx) {
+        A.init_fetch(wave, lane, a.N * EB, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
+        B.init_fetch(w + (size_t)t.j0 * EB, a.ldw * EB, t.nc, t.nj * EB);
+      } else {
+        A.init_fetch(y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.nc, t.ni * EB);
+        B.init_fetch(x + ((size_t)(GATHER ? 0 : t.p0) * a.ldx + t.j0) * EB, a.ldx * EB, t.nc, t.nj * EB);
+      }
+    } else if constexpr (OP == kOpY) {
       const unsigned cb = (unsigned)a.K * EB;
       if (a.perm_src)
         A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb, [&](int r) -> unsigned {
@@ -292,14 +392,14 @@ struct TileKernel {
       if constexpr (IDX) {
         const __attribute__((address_space(4))) int* p = (const __attribute__((address_space(4))) int*)a.perm_src + t.p0;
 #pragma unroll
-        for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * kStageRows + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
+        for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
       }
     };
     auto idx_rows = [&](int s) {
 #pragma unroll
       for (int n = 0; n < NX; ++n) {
         const int v = idx_next[n], r = div_k(v, a.k, magic);
-        const bool ok = v >= 0 && r < a.x_rows && s * kStageRows + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
+        const bool ok = v >= 0 && r < a.x_rows && s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
         idx[n] = ok ? (unsigned)r * ldx : kOutside;
       }
     };
@@ -332,6 +432,39 @@ struct TileKernel {
     };
     constexpr int NL = OpA::LQ + OpB::LQ;
 
+    // STAGED: a stage in registers, and from there to its buffer
+    u32x4 held[STAGED ? NL : 1];
+    int fetched = 0;  // stages
+    auto fetch = [&] {
+#pragma unroll
+      for (int q = 0; q < OpA::LQ; ++q) {
+        if constexpr (SA) held[q] = A.fetch(q, wave, lane);
+        else held[q] = A.fetch(q);
+      }
+#pragma unroll
+      for (int q = 0; q < OpB::LQ; ++q) {
+        if constexpr (GATHER && OP == kOpDw) {
+          const int c = fetched * KE + OpB::c_row(q, wave, lane), o = (int)OpB::col_of(q, wave, lane);
+          const int xr = c < t.nc ? x_row(a, t.p0 + c) : -1;
+          held[OpA::LQ + q] = load_part<EB>(x + ((size_t)max(xr, 0) * a.ldx + t.j0) * EB + o, xr >= 0 ? t.nj * EB - o : 0);
+        } else if constexpr (SB) {
+          held[OpA::LQ + q] = B.fetch(q, wave, lane);
+        } else {
+          held[OpA::LQ + q] = B.fetch(q);
+        }
+      }
+      A.end_fetch();
+      B.end_fetch();
+      ++fetched;
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int L = 0; L < NL; ++L) {
+        const lptr l = lds + buf * STAGE + (L < OpA::LQ ? 0 : OpA::BYTES) + ((L < OpA::LQ ? L : L - OpA::LQ) * kWaves + wave) * 1024;
+        *(__attribute__((address_space(3))) u32x4*)(l + lane * 16) = held[L];
+      }
+    };
+
     // ---- fragments.  Row fragments of wave row wi: 2 f + wi; column fragments of wave column wj: WJ wj + f
     int addr_a, addr_b;
     if constexpr (SA) addr_a = OpA::lane_addr(wi, lane);
@@ -340,12 +473,12 @@ struct TileKernel {
     else addr_b = OpB::lane_addr(16 * WJ * wj, lane);
     auto read_a = [&](int f, int buf, int h) -> Frag {
       const lptr l = lds + buf * STAGE;
-      if constexpr (SA) return OpA::read(l, addr_a, 2 * f, h);
+      if constexpr (SA) return OpA::template read<Frag>(l, addr_a, 2 * f, h);
       else return OpA::template read<Frag>(l, addr_a, 2 * f, h);
     };
     auto read_b = [&](int f, int buf, int h) -> Frag {
       const lptr l = lds + buf * STAGE + OpA::BYTES;
-      if constexpr (SB) return OpB::read(l, addr_b, f, h);
+      if constexpr (SB) return OpB::template read<Frag>(l, addr_b, f, h);
       else return OpB::template read<Frag>(l, addr_b, f, h);
     };
 
@@ -358,19 +491,25 @@ struct TileKernel {
     // ---- prologue: the first two stages, the fragments of step 0
     const int ns = (t.nc + KE - 1) / KE;  // >= 1
     {
+      if constexpr (STAGED) {
+        fetch();
+        put(0);
+        fetch();
+      } else {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if constexpr (IDX) {
-          idx_load(s);
-          idx_rows(s);
+        for (int s = 0; s < 2; ++s) {
+          if constexpr (IDX) {
+            idx_load(s);
+            idx_rows(s);
+          }
+          begin_stage();
+          static_for<NL>([&](auto Lc) { load_now(load(Lc, s)); });
+          end_stage();
         }
-        begin_stage();
-        static_for<NL>([&](auto Lc) { load_now(load(Lc, s)); });
-        end_stage();
+        idx_load(2);
+        wait_loads<NL>();
       }
-      idx_load(2);
       Frag fa[2][NI], fb[2][WJ];
-      wait_loads<NL>();
       barrier_keep_loads();
 #pragma unroll
       for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0, 0);
@@ -384,8 +523,9 @@ struct TileKernel {
         constexpr int h = hc;
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         if constexpr (h == 1) {
-          wait_loads<0>();
+          if constexpr (!STAGED) wait_loads<0>();
           barrier_keep_loads();
+          if constexpr (STAGED) fetch();
           if constexpr (IDX) {
             idx_rows(s + 2);
             idx_load(s + 3);
@@ -394,14 +534,14 @@ struct TileKernel {
         __builtin_amdgcn_sched_barrier(0);
         const int cbuf = s & 1, rbuf = h == 0 ? cbuf : cbuf ^ 1;
         // slots: reads over the first three quarters of the MFMAs, loads over the first half
-        constexpr int R = WJ * NI, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
-        constexpr int NQ = h == 1 ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
+        constexpr int R = WJ * NI * TT::MPF, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
+        constexpr int NQ = h == 1 && !STAGED ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
         static_for<R>([&](auto rc) {
-          constexpr int r = rc, j = r / NI, i = r % NI;
+          constexpr int r = rc, e = r / (WJ * NI), j = r % (WJ * NI) / NI, i = r % NI;
           constexpr int l0 = spread_lo(r, NQ, TL), l1 = r < TL ? spread_hi(r, NQ, TL) : l0;
           if constexpr (l0 == 0 && l1 > 0) begin_stage();
-          if constexpr (l1 > l0) tile_mfma(acc[j][i], fb[h][j], fa[h][i], load(std::integral_constant<int, l0>{}, cbuf));
-          else tile_mfma(acc[j][i], fb[h][j], fa[h][i]);
+          if constexpr (l1 > l0) tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i], load(std::integral_constant<int, l0>{}, cbuf));
+          else tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i]);
           static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) {
             load_now(load(std::integral_constant<int, l0 + 1 + Lc>{}, cbuf));
           });
@@ -414,13 +554,14 @@ struct TileKernel {
           });
           __builtin_amdgcn_sched_barrier(0);
         });
+        if constexpr (STAGED && h == 0) put(cbuf ^ 1);  // free since the barrier of the stage before
       };
       int s = 0;
       do {
         step(std::integral_constant<int, 0>{}, s);
         step(std::integral_constant<int, 1>{}, s);
       } while (++s < ns);
-      wait_loads<0>();  // nothing may land in LDS once the workgroup is gone
+      if constexpr (!STAGED) wait_loads<0>();  // nothing may land in LDS once the workgroup is gone
     }
 
     // ---- results.  The accumulators pass an empty asm after the wait states, so that no read of them can be
@@ -513,9 +654,9 @@ __device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, in
   row = band * kBand + r - col * h;
 }
 
-template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
 __global__ __launch_bounds__(256, (WI * WJ > 16 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
-  typedef TileKernel<OP, TYPE, WI, WJ, GATHER> Tk;
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED> Tk;
   extern __shared__ __align__(1024) char smem[];
   const int nj = OP == kOpY ? a.N : a.K, ncol = (nj + Tk::BJ - 1) / Tk::BJ;
   TileItem t;
@@ -524,12 +665,21 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 ? 1 : 2)) void grouped_tile_kern
   if constexpr (OP == kOpDw) {
     const int nt = (a.N + Tk::BI - 1) / Tk::BI;
     const int per = (int)((gridDim.x + kXcds - 1) / kXcds);  // the grid is a multiple of the XCDs
-    const long long u = (long long)xcd * per + local;
-    if (u >= (long long)a.E * nt * ncol) return;
+    long long u = (long long)xcd * per + local;
+    const long long tiles = (long long)a.E * nt * ncol;
+    if (u >= tiles * a.split) return;
+    const int part = __builtin_amdgcn_readfirstlane((int)(u / tiles));
+    u -= part * tiles;
+    if (a.split > 1) a.w = (const char*)a.w + (size_t)part * a.E * a.w_stride * 4;
     t.e = __builtin_amdgcn_readfirstlane((int)(u / ((long long)nt * ncol)));
     band_order((int)(u - (long long)t.e * nt * ncol), nt, ncol, row, col);
     const int2 g = group_range(a.offsets, t.e, a.rows);
     t.p0 = g.x, t.nc = g.y;
+    if (a.split > 1) {  // this part of the group's rows, in whole stages
+      const int len = (g.y + a.split * Tk::KE - 1) / (a.split * Tk::KE) * Tk::KE;
+      const int from = min(part * len, g.y);
+      t.p0 += from, t.nc = min(len, g.y - from);
+    }
     t.i0 = row * Tk::BI;
     t.ni = min(Tk::BI, a.N - t.i0);
   } else {
@@ -566,25 +716,27 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 ? 1 : 2)) void grouped_tile_kern
   });
 }
 
-template <int OP, int TYPE, int WI, int WJ, bool GATHER>
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
 int tile_launch_one(const GroupArgs& a, hipStream_t s) {
-  typedef TileKernel<OP, TYPE, WI, WJ, GATHER> Tk;
-  static bool attr_set[64];  // per device
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (!attr_set[dev]) {
-    hipError_t e = hipFuncSetAttribute((const void*)grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER>,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)Tk::LDS);
-    if (e != hipSuccess) return hip_fail(e, "moe_grouped_gemm: LDS attribute");
-    attr_set[dev] = true;
-  }
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED> Tk;
   const int nj = OP == kOpY ? a.N : a.K;
-  const long long nt = OP == kOpDw ? (long long)a.E * ((a.N + Tk::BI - 1) / Tk::BI) : group_tiles_max(a.rows, a.E, Tk::BI);
+  const long long nt = OP == kOpDw ? (long long)a.E * ((a.N + Tk::BI - 1) / Tk::BI) * a.split
+                                   : group_tiles_max(a.rows, a.E, Tk::BI);
   long long nb = nt * ((nj + Tk::BJ - 1) / Tk::BJ);
   if (nb == 0) return MOE_OK;
   nb = (nb + kXcds - 1) / kXcds * kXcds;
   if (nb > kMaxThreads / 256) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
-  hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER>), dim3((unsigned)nb), dim3(256), Tk::LDS, s, a);
+  static bool attr_set[64];  // per device
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (!attr_set[dev]) {
+    hipError_t e = hipFuncSetAttribute((const void*)grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)Tk::LDS);
+    if (e != hipSuccess) return hip_fail(e, "moe_grouped_gemm: LDS attribute");
+    attr_set[dev] = true;
+  }
+  hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED>), dim3((unsigned)nb), dim3(256), Tk::LDS, s,
+                     a);
   MOE_CHECK_LAUNCH("moe_grouped_gemm launch");
   return MOE_OK;
 }
