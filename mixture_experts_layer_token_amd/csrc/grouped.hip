@@ -44,6 +44,12 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   const bool aw = op == kOpDw || (al(a.w, a.ldw) && a.w_stride * eb % 16 == 0 && a.K * eb % 16 == 0);
   const bool ay = op == kOpY || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
   TileShape t = ax && aw && ay && tile_spans_fit(a, op, eb) ? kLarge : kStaged;
+  if (op == kOpY) {
+    // few rows and few tiles: the kernel that spreads each expert's features over N / 16 workgroups
+    const long long groups = a.rows < a.E ? a.rows : a.E;
+    if ((a.rows + a.E - 1) / a.E <= 64 && groups * ((a.N + 127) / 128) < 512)
+      return launch_grouped_decode(a, type, t == kLarge, s);
+  }
   if (op == kOpDw) {
     const int split = dw_split(a.rows, a.N, a.K, a.E);
     if (split > 1) {

@@ -30,35 +30,10 @@
 
 #include "grouped.hpp"
 #include "mfma_pipe.hpp"
+#include "operand.hpp"
 
 namespace moe {
 namespace {
-
-typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
-typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
-
-template <int TYPE>
-struct TileT;
-template <>
-struct TileT<kBf16> {
-  typedef bf16x8 Frag;
-  typedef f32x4 Acc;
-  static constexpr int EB = 2, MPF = 1;  // bytes of an element, MFMAs per pair of fragments
-};
-template <>
-struct TileT<kI8> {
-  typedef i32x4 Frag;
-  typedef i32x4 Acc;
-  static constexpr int EB = 1, MPF = 1;
-};
-// An fp32 fragment is 16 bytes of c per lane as well: lane group g (lane / 16) holds c = 4 g .. 4 g + 3, and MFMA e takes
-// element e of every lane, that is c = e, 4 + e, 8 + e, 12 + e.
-template <>
-struct TileT<kF32> {
-  typedef f32x4 Frag;
-  typedef f32x4 Acc;
-  static constexpr int EB = 4, MPF = 4;
-};
 
 // Waits until at most N of this wave's loads are in flight (the compiler does not know the ones in inline assembly)
 template <int N>
@@ -89,7 +64,6 @@ constexpr int kWaves = 4;
 // Operands are read through buffer descriptors with an exact length: a lane whose offset lies past the end
 // gets zeros, which is how everything outside an operand (the end of c, rows of zeros) enters the LDS as
 // zeros with no work per load.  The base advances by scalar arithmetic, the lanes' 32-bit offsets stay.
-constexpr unsigned kOutside = 0xFFFFFC00u;      // offset past the end of every descriptor, also with a row's bytes added
 
 // The loads are inline assembly (they have no result register: the data goes to LDS): after the compiler's own
 // LDS-direct loads, every transposing LDS read would wait for all loads in flight.  `Load` is one of them, kept
@@ -123,22 +97,6 @@ template <int E>
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const f32x4& b, const f32x4& a, const Load& d) {
   asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x4_f32 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
                : "+a"(acc) : "v"(b[E]), "v"(a[E]), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
-}
-
-// 16 bytes at any element-aligned address, of which the first n exist (the others are zeros)
-template <int EB>
-__device__ __forceinline__ u32x4 load_part(gptr p, int n) {
-  typedef u32x4 __attribute__((aligned(1))) any4;
-  typedef typename std::conditional<EB == 1, unsigned char, typename std::conditional<EB == 2, unsigned short, unsigned>::type>::type El;
-  u32x4 v = {0, 0, 0, 0};
-  if (n >= 16) {
-    v = *(const __attribute__((address_space(1))) any4*)p;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16 / EB; ++i)
-      if (i * EB < n) v[i * EB / 4] |= (unsigned)((const __attribute__((address_space(1))) El*)p)[i] << (i * EB % 4 * 8);
-  }
-  return v;
 }
 
 // One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; fragments
