@@ -53,7 +53,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   if (op == kOpDw) {
     const int split = dw_split(a.rows, a.N, a.K, a.E);
     if (split > 1) {
-      if (t == kLarge) t = kSmall;
+      if (t == kLarge) t = kDeep;
       GroupArgs p = a;
       p.split = split;
       p.w = ws, p.ldw = a.K, p.w_stride = (long long)a.N * a.K, p.out_bf16 = 0;
@@ -71,7 +71,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     // Row counts are known on average only.
     const long long ni = op == kOpDw ? a.N : (a.rows + a.E - 1) / a.E, nj = op == kOpY ? a.N : a.K;
     auto tiles = [&](long long b) { return (long long)a.E * ((ni + b - 1) / b) * ((nj + b - 1) / b); };
-    if (tiles(256) < 256) t = kSmall;
+    if (tiles(256) < 256) t = tiles(128) <= 256 ? kDeep : kSmall;
   }
   if (type == kF32) return launch_tile_f32(a, op, t, s);
   if (type == kI8) return launch_tile_y_i8(a, t, s);

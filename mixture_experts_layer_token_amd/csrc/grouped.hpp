@@ -109,9 +109,10 @@ inline bool tile_spans_fit(const GroupArgs& a, int op, int eb) {
   return (op == kOpDx || x) && (op == kOpDw || rows(256, a.ldw)) && (op == kOpY || rows(256, a.ldy));
 }
 
-// grouped_tile_*.hip: the MFMA tile kernel.  kLarge: 256 x 256 results per workgroup (bf16, int8), kSmall: 128 x 128, both
-// for rows on 16-byte boundaries and spans that fit; kStaged: 128 x 128 for any others.
-enum TileShape { kLarge, kSmall, kStaged };
+// grouped_tile_*.hip: the MFMA tile kernel.  kLarge: 256 x 256 results per workgroup (bf16, int8), kSmall: 128 x 128;
+// kDeep: 128 x 128 with four stages in LDS instead of two; these for rows on 16-byte boundaries and spans that fit;
+// kStaged: 128 x 128 for any others.
+enum TileShape { kLarge, kSmall, kDeep, kStaged };
 int launch_tile_y_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_y_i8(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_dx_bf16(const GroupArgs& a, TileShape t, hipStream_t s);

@@ -28,6 +28,8 @@
 //    columns past the edge repeat valid ones and are not stored.
 #pragma once
 
+#include <algorithm>
+
 #include "grouped.hpp"
 #include "mfma_pipe.hpp"
 #include "operand.hpp"
@@ -256,8 +258,8 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
 
 // 16 rows of w columns from a wave's LDS region, of which ni rows and nj columns exist; they start at row i0, column
 // j0 of the tile.  Element by element: the rare layouts take it.
-__device__ __forceinline__ void store_rows(const float* reg, char* out, long long ldc, int ni, int nj, int i0,
-                                                     int j0, int w, const float* sw, int bf16) {
+__device__ __forceinline__ void store_rows(const __attribute__((address_space(3))) float* reg, char* out, long long ldc,
+                                           int ni, int nj, int i0, int j0, int w, const float* sw, int bf16) {
   const int lane = threadIdx.x & 63;
 #pragma unroll 1
   for (int r = 0; r < min(ni, 16); ++r)
@@ -271,14 +273,15 @@ __device__ __forceinline__ void store_rows(const float* reg, char* out, long lon
 // ------------------------------------------------------------------ tiles
 struct TileItem {
   int e, i0, ni, j0, nj, p0, nc;  // expert; first i and j and how many exist; first grouped row; length of c
+  int part;                       // weights' gradient: part of the group's rows
 };
 
 // Division of a grouped pair's flat index by k (2 <= k <= 16, index below 2^28): multiplication by ceil(2^32 / k),
 // off by less than 1 / k there.
 __device__ __forceinline__ int div_k(int s, int k, unsigned magic) { return k == 1 ? s : (int)__umulhi((unsigned)s, magic); }
 
-// STAGED: operands pass through registers (any alignment, stride and extent)
-template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
+// STAGED: operands pass through registers (any alignment, stride and extent).  NB: stages in LDS.
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
 struct TileKernel {
   typedef TileT<TYPE> TT;
   typedef typename TT::Frag Frag;
@@ -289,111 +292,138 @@ struct TileKernel {
   typedef typename std::conditional<SA, Strided<BI, EB>, Contig<BI, EB>>::type OpA;
   typedef typename std::conditional<SB, Strided<BJ, EB>, Contig<BJ, EB>>::type OpB;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
-  static constexpr size_t LDS = (size_t)2 * STAGE;
+  static constexpr int NL = OpA::LQ + OpB::LQ;           // loads per stage and wave
+  static constexpr int REGION = 16 * 16 * WJ * 4;        // per wave, behind the stages: see store_rows
+  static constexpr size_t LDS = (size_t)NB * STAGE + kWaves * REGION;
   static constexpr bool IDX = GATHER && OP == kOpDw && !STAGED;  // x rows of c through perm_src
   static constexpr int RPL = IDX ? 1024 / (BJ * EB) : 1;  // c rows per load of B
+  static constexpr int NX = IDX ? OpB::LQ * RPL : 1;
+  // A workgroup walks over several tiles, the next one's first loads under way while a tile's results are written; not
+  // with accumulators that fill the register file: the compiler then moves some of them around inside the loop.
+  static constexpr bool WALK = WI * WJ <= 16;
+  static_assert(NB == 2 || (NB == 4 && !STAGED), "stages");
 
-  // One tile with NI row fragments per wave.
-  template <int NI>
-  static __device__ __forceinline__ void body(const GroupArgs& a, const TileItem& t, lptr lds) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wi = wave >> 1, wj = wave & 1;
-    const unsigned magic = a.k > 1 ? (unsigned)((0x100000000ULL + a.k - 1) / a.k) : 0;
-
-    // ---- operands
+  // The operands of one tile on their way to LDS.
+  struct Feed {
+    const GroupArgs& a;
+    const int lane, wave;
+    const lptr lds;
+    const unsigned magic;
+    TileItem t;
     OpA A;
     OpB B;
-    const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
-    const unsigned ldx = (unsigned)a.ldx * EB, ldw = (unsigned)a.ldw * EB, ldy = (unsigned)a.ldy * EB;
-    if constexpr (STAGED) {
-      if constexpr (OP == kOpY) {
-        A.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr {
-          const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
-          return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
-        });
-        B.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
-      } else if constexpr (OP == kOpDx) {
-        A.init_fetch(wave, lane, a.N * EB, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
-        B.init_fetch(w + (size_t)t.j0 * EB, a.ldw * EB, t.nc, t.nj * EB);
-      } else {
-        A.init_fetch(y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.nc, t.ni * EB);
-        B.init_fetch(x + ((size_t)(GATHER ? 0 : t.p0) * a.ldx + t.j0) * EB, a.ldx * EB, t.nc, t.nj * EB);
-      }
-    } else if constexpr (OP == kOpY) {
-      const unsigned cb = (unsigned)a.K * EB;
-      if (a.perm_src)
-        A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb, [&](int r) -> unsigned {
-          const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
-          return xr >= 0 ? (unsigned)xr * ldx : kOutside;
-        });
-      else
-        A.init(wave, lane, x + (size_t)t.p0 * a.ldx * EB, (unsigned)(t.ni - 1) * ldx + cb, cb,
-               [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
-      B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1) * ldw + cb, cb,
-             [&](int r) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
-    } else if constexpr (OP == kOpDx) {
-      const unsigned cb = (unsigned)a.N * EB;
-      A.init(wave, lane, y + (size_t)t.p0 * a.ldy * EB, (unsigned)(t.ni - 1) * ldy + cb, cb,
-             [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
-      B.init(wave, lane, w + (size_t)t.j0 * EB, ldw, t.nc, t.nj * EB);
-    } else {
-      A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, ldy, t.nc, t.ni * EB);
-      if constexpr (!IDX) B.init(wave, lane, x + ((size_t)t.p0 * a.ldx + t.j0) * EB, ldx, t.nc, t.nj * EB);
-    }
     // IDX: perm_src of this wave's c rows of a stage, by scalar loads one stage ahead, and the offsets of the x rows
     // they name for the stage to be loaded next (kOutside: zeros)
-    constexpr int NX = IDX ? OpB::LQ * RPL : 1;
     int idx_next[NX];
     unsigned idx[NX], bcol[OpB::LQ];
-    auto idx_load = [&](int s) {
+    // STAGED: a stage in registers
+    u32x4 held[STAGED ? NL : 1];
+    int fetched;  // stages
+
+    __device__ __forceinline__ Feed(const GroupArgs& args, lptr smem)
+        : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lds(smem),
+          magic(args.k > 1 ? (unsigned)((0x100000000ULL + args.k - 1) / args.k) : 0) {}
+
+    __device__ __forceinline__ void init(const TileItem& item) {
+      t = item;
+      const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
+      const unsigned ldx = (unsigned)a.ldx * EB, ldw = (unsigned)a.ldw * EB, ldy = (unsigned)a.ldy * EB;
+      if constexpr (STAGED) {
+        fetched = 0;
+        if constexpr (OP == kOpY) {
+          A.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr {
+            const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
+            return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
+          });
+          B.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
+        } else if constexpr (OP == kOpDx) {
+          A.init_fetch(wave, lane, a.N * EB, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
+          B.init_fetch(w + (size_t)t.j0 * EB, a.ldw * EB, t.nc, t.nj * EB);
+        } else {
+          A.init_fetch(y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.nc, t.ni * EB);
+          B.init_fetch(x + ((size_t)(GATHER ? 0 : t.p0) * a.ldx + t.j0) * EB, a.ldx * EB, t.nc, t.nj * EB);
+        }
+      } else if constexpr (OP == kOpY) {
+        const unsigned cb = (unsigned)a.K * EB;
+        if (a.perm_src)
+          A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb, [&](int r) -> unsigned {
+            const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
+            return xr >= 0 ? (unsigned)xr * ldx : kOutside;
+          });
+        else
+          A.init(wave, lane, x + (size_t)t.p0 * a.ldx * EB, (unsigned)(t.ni - 1) * ldx + cb, cb,
+                 [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
+        B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1) * ldw + cb, cb,
+               [&](int r) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
+      } else if constexpr (OP == kOpDx) {
+        const unsigned cb = (unsigned)a.N * EB;
+        A.init(wave, lane, y + (size_t)t.p0 * a.ldy * EB, (unsigned)(t.ni - 1) * ldy + cb, cb,
+               [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
+        B.init(wave, lane, w + (size_t)t.j0 * EB, ldw, t.nc, t.nj * EB);
+      } else {
+        A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, ldy, t.nc, t.ni * EB);
+        if constexpr (!IDX) B.init(wave, lane, x + ((size_t)t.p0 * a.ldx + t.j0) * EB, ldx, t.nc, t.nj * EB);
+      }
+      if constexpr (IDX) {
+#pragma unroll
+        for (int q = 0; q < OpB::LQ; ++q) bcol[q] = OpB::col(q, wave, lane, t.nj * EB);
+      }
+    }
+    __device__ __forceinline__ void idx_load(int s) {
       if constexpr (IDX) {
         const __attribute__((address_space(4))) int* p = (const __attribute__((address_space(4))) int*)a.perm_src + t.p0;
 #pragma unroll
         for (int n = 0; n < NX; ++n) idx_next[n] = p[min(s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL, t.nc - 1)];
       }
-    };
-    auto idx_rows = [&](int s) {
+    }
+    __device__ __forceinline__ void idx_rows(int s) {
+      if constexpr (IDX) {
 #pragma unroll
-      for (int n = 0; n < NX; ++n) {
-        const int v = idx_next[n], r = div_k(v, a.k, magic);
-        const bool ok = v >= 0 && r < a.x_rows && s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
-        idx[n] = ok ? (unsigned)r * ldx : kOutside;
+        for (int n = 0; n < NX; ++n) {
+          const int v = idx_next[n], r = div_k(v, a.k, magic);
+          const bool ok = v >= 0 && r < a.x_rows && s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
+          idx[n] = ok ? (unsigned)r * (unsigned)a.ldx * EB : kOutside;
+        }
       }
-    };
-    auto load_b_gather = [&](auto qc, lptr l) -> Load {
-      constexpr int q = qc;
-      unsigned o = idx[(q * RPL) % NX];
-      static_for<RPL - 1>([&](auto ic) { o = lane / (64 / RPL) == ic + 1 ? idx[(q * RPL + ic + 1) % NX] : o; });
-      return make_load(x + (size_t)t.j0 * EB, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + (unsigned)t.nj * EB : 0,
-                       o + bcol[q], l + (q * kWaves + wave) * 1024);
-    };
-    if constexpr (IDX) {
-#pragma unroll
-      for (int q = 0; q < OpB::LQ; ++q) bcol[q] = OpB::col(q, wave, lane, t.nj * EB);
     }
     // the loads of the stage to be loaded next, into buffer buf: begin, load L = 0 .. NL-1, end
-    auto begin_stage = [&] {
+    __device__ __forceinline__ void begin_stage() {
       A.begin_stage();
       if constexpr (!IDX) B.begin_stage();
-    };
-    auto load = [&](auto Lc, int buf) -> Load {
-      constexpr int L = Lc;
+    }
+    template <int L>
+    __device__ __forceinline__ Load load(int buf) {
       const lptr la = lds + buf * STAGE, lb = la + OpA::BYTES;
-      if constexpr (L < OpA::LQ) return A.load(L, la, wave);
-      else if constexpr (IDX) return load_b_gather(std::integral_constant<int, L - OpA::LQ>{}, lb);
-      else return B.load(L - OpA::LQ, lb, wave);
-    };
-    auto end_stage = [&] {
+      if constexpr (L < OpA::LQ) {
+        return A.load(L, la, wave);
+      } else if constexpr (IDX) {
+        constexpr int q = L - OpA::LQ;
+        unsigned o = idx[(q * RPL) % NX];
+        static_for<RPL - 1>([&](auto ic) { o = lane / (64 / RPL) == ic + 1 ? idx[(q * RPL + ic + 1) % NX] : o; });
+        const unsigned span = a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * (unsigned)a.ldx * EB + (unsigned)t.nj * EB : 0;
+        return make_load((gptr)a.x + (size_t)t.j0 * EB, span, o + bcol[q], lb + (q * kWaves + wave) * 1024);
+      } else {
+        return B.load(L - OpA::LQ, lb, wave);
+      }
+    }
+    __device__ __forceinline__ void end_stage() {
       A.end_stage();
       if constexpr (!IDX) B.end_stage();
-    };
-    constexpr int NL = OpA::LQ + OpB::LQ;
+    }
+    // the first NB stages
+    __device__ __forceinline__ void prologue() {
+#pragma unroll
+      for (int s = 0; s < NB; ++s) {
+        idx_load(s);
+        idx_rows(s);
+        begin_stage();
+        static_for<NL>([&](auto Lc) { load_now(load<Lc>(s)); });
+        end_stage();
+      }
+      idx_load(NB);
+    }
 
-    // STAGED: a stage in registers, and from there to its buffer
-    u32x4 held[STAGED ? NL : 1];
-    int fetched = 0;  // stages
-    auto fetch = [&] {
+    __device__ __forceinline__ void fetch() {
 #pragma unroll
       for (int q = 0; q < OpA::LQ; ++q) {
         if constexpr (SA) held[q] = A.fetch(q, wave, lane);
@@ -404,7 +434,8 @@ struct TileKernel {
         if constexpr (GATHER && OP == kOpDw) {
           const int c = fetched * KE + OpB::c_row(q, wave, lane), o = (int)OpB::col_of(q, wave, lane);
           const int xr = c < t.nc ? x_row(a, t.p0 + c) : -1;
-          held[OpA::LQ + q] = load_part<EB>(x + ((size_t)max(xr, 0) * a.ldx + t.j0) * EB + o, xr >= 0 ? t.nj * EB - o : 0);
+          held[OpA::LQ + q] =
+              load_part<EB>((gptr)a.x + ((size_t)max(xr, 0) * a.ldx + t.j0) * EB + o, xr >= 0 ? t.nj * EB - o : 0);
         } else if constexpr (SB) {
           held[OpA::LQ + q] = B.fetch(q, wave, lane);
         } else {
@@ -414,138 +445,133 @@ struct TileKernel {
       A.end_fetch();
       B.end_fetch();
       ++fetched;
-    };
-    auto put = [&](int buf) {
+    }
+    __device__ __forceinline__ void put(int buf) {
 #pragma unroll
       for (int L = 0; L < NL; ++L) {
-        const lptr l = lds + buf * STAGE + (L < OpA::LQ ? 0 : OpA::BYTES) + ((L < OpA::LQ ? L : L - OpA::LQ) * kWaves + wave) * 1024;
+        const lptr l =
+            lds + buf * STAGE + (L < OpA::LQ ? 0 : OpA::BYTES) + ((L < OpA::LQ ? L : L - OpA::LQ) * kWaves + wave) * 1024;
         *(__attribute__((address_space(3))) u32x4*)(l + lane * 16) = held[L];
       }
-    };
+    }
+  };
 
+  // One tile with NI row fragments per wave.  Its first NB stages have landed for this wave (STAGED: feed is
+  // initialised).  advance() is called when the tile's last operands have been read: it starts the loads of the
+  // workgroup's next tile, which land while this tile's results are written.
+  template <int NI, typename F>
+  static __device__ __forceinline__ void body(const GroupArgs& a, const TileItem& t, Feed& feed, F&& advance) {
+    const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
+    const lptr lds = feed.lds;
     // ---- fragments.  Row fragments of wave row wi: 2 f + wi; column fragments of wave column wj: WJ wj + f
     int addr_a, addr_b;
     if constexpr (SA) addr_a = OpA::lane_addr(wi, lane);
     else addr_a = OpA::lane_addr(16 * wi, lane);
     if constexpr (SB) addr_b = OpB::lane_addr(WJ * wj, lane);
     else addr_b = OpB::lane_addr(16 * WJ * wj, lane);
-    auto read_a = [&](int f, int buf, int h) -> Frag {
-      const lptr l = lds + buf * STAGE;
-      if constexpr (SA) return OpA::template read<Frag>(l, addr_a, 2 * f, h);
-      else return OpA::template read<Frag>(l, addr_a, 2 * f, h);
-    };
-    auto read_b = [&](int f, int buf, int h) -> Frag {
-      const lptr l = lds + buf * STAGE + OpA::BYTES;
-      if constexpr (SB) return OpB::template read<Frag>(l, addr_b, f, h);
-      else return OpB::template read<Frag>(l, addr_b, f, h);
+    auto read_a = [&](int f, int buf, int h) { return OpA::template read<Frag>(lds + buf * STAGE, addr_a, 2 * f, h); };
+    auto read_b = [&](int f, int buf, int h) {
+      return OpB::template read<Frag>(lds + buf * STAGE + OpA::BYTES, addr_b, f, h);
     };
 
     Acc acc[WJ][NI];
 #pragma unroll
     for (int j = 0; j < WJ; ++j)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) acc[j][i] = Acc{};
-
-    // ---- prologue: the first two stages, the fragments of step 0
-    const int ns = (t.nc + KE - 1) / KE;  // >= 1
-    {
-      if constexpr (STAGED) {
-        fetch();
-        put(0);
-        fetch();
-      } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if constexpr (IDX) {
-            idx_load(s);
-            idx_rows(s);
-          }
-          begin_stage();
-          static_for<NL>([&](auto Lc) { load_now(load(Lc, s)); });
-          end_stage();
-        }
-        idx_load(2);
-        wait_loads<NL>();
+      for (int i = 0; i < NI; ++i) {
+        acc[j][i] = Acc{};
+        asm volatile("" : "+a"(acc[j][i]));  // (written here, two wait states before the first MFMA at least)
       }
-      Frag fa[2][NI], fb[2][WJ];
-      barrier_keep_loads();
-#pragma unroll
-      for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0, 0);
-#pragma unroll
-      for (int j = 0; j < WJ; ++j) fb[0][j] = read_b(j, 0, 0);
 
-      // ---- one MFMA step: step h of stage s is multiplied, the next one's fragments are read.  With h = 1 the
-      // barrier comes first: it publishes stage s+1 (every wave has waited for its own loads of it) and frees the
-      // buffer of stage s (its last fragments are in registers), into which stage s+2 is then loaded.
-      auto step = [&](auto hc, int s) {
-        constexpr int h = hc;
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        if constexpr (h == 1) {
-          if constexpr (!STAGED) wait_loads<0>();
-          barrier_keep_loads();
-          if constexpr (STAGED) fetch();
-          if constexpr (IDX) {
-            idx_rows(s + 2);
-            idx_load(s + 3);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        const int cbuf = s & 1, rbuf = h == 0 ? cbuf : cbuf ^ 1;
-        // slots: reads over the first three quarters of the MFMAs, loads over the first half
-        constexpr int R = WJ * NI * TT::MPF, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
-        constexpr int NQ = h == 1 && !STAGED ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
-        static_for<R>([&](auto rc) {
-          constexpr int r = rc, e = r / (WJ * NI), j = r % (WJ * NI) / NI, i = r % NI;
-          constexpr int l0 = spread_lo(r, NQ, TL), l1 = r < TL ? spread_hi(r, NQ, TL) : l0;
-          if constexpr (l0 == 0 && l1 > 0) begin_stage();
-          if constexpr (l1 > l0) tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i], load(std::integral_constant<int, l0>{}, cbuf));
-          else tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i]);
-          static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) {
-            load_now(load(std::integral_constant<int, l0 + 1 + Lc>{}, cbuf));
-          });
-          if constexpr (l1 > l0 && l1 == NQ) end_stage();
-          constexpr int lo = spread_lo(r, NR, T), hi = r < T ? spread_hi(r, NR, T) : lo;
-          static_for<hi - lo>([&](auto mc) {
-            constexpr int m = lo + mc;
-            if constexpr (m < NI) fa[h ^ 1][m] = read_a(m, rbuf, h ^ 1);
-            else fb[h ^ 1][m - NI] = read_b(m - NI, rbuf, h ^ 1);
-          });
-          __builtin_amdgcn_sched_barrier(0);
-        });
-        if constexpr (STAGED && h == 0) put(cbuf ^ 1);  // free since the barrier of the stage before
-      };
-      int s = 0;
-      do {
-        step(std::integral_constant<int, 0>{}, s);
-        step(std::integral_constant<int, 1>{}, s);
-      } while (++s < ns);
-      if constexpr (!STAGED) wait_loads<0>();  // nothing may land in LDS once the workgroup is gone
+    const int ns = (t.nc + KE - 1) / KE;  // >= 1
+    if constexpr (STAGED) {
+      feed.fetch();
+      barrier_keep_loads();  // every wave is done with the buffers of the tile before
+      feed.put(0);
+      feed.fetch();
     }
+    Frag fa[2][NI], fb[2][WJ];
+    barrier_keep_loads();
+#pragma unroll
+    for (int i = 0; i < NI; ++i) fa[0][i] = read_a(i, 0, 0);
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) fb[0][j] = read_b(j, 0, 0);
 
-    // ---- results.  The accumulators pass an empty asm after the wait states, so that no read of them can be
-    // scheduled before.
+    // ---- one MFMA step: step h of stage s is multiplied, the next one's fragments are read.  With h = 1 the
+    // barrier comes first: it publishes stage s+1 (every wave has waited for its own loads of it) and frees the
+    // buffer of stage s (its last fragments are in registers), into which stage s+NB is then loaded.
+    auto step = [&](auto hc, int s) {
+      constexpr int h = hc;
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      if constexpr (h == 1) {
+        // (stage 1 landed before the tile began; a wait there would be one for the last tile's stores)
+        if constexpr (!STAGED)
+          if (s > 0) wait_loads<(NB - 2) * NL>();
+        barrier_keep_loads();
+        if constexpr (STAGED) feed.fetch();
+        feed.idx_rows(s + NB);
+        feed.idx_load(s + NB + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const int cbuf = s & (NB - 1), nbuf = (s + 1) & (NB - 1), rbuf = h == 0 ? cbuf : nbuf;
+      // slots: reads over the first three quarters of the MFMAs, loads over the first half
+      constexpr int R = WJ * NI * TT::MPF, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
+      constexpr int NQ = h == 1 && !STAGED ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
+      static_for<R>([&](auto rc) {
+        constexpr int r = rc, e = r / (WJ * NI), j = r % (WJ * NI) / NI, i = r % NI;
+        constexpr int l0 = spread_lo(r, NQ, TL), l1 = r < TL ? spread_hi(r, NQ, TL) : l0;
+        if constexpr (l0 == 0 && l1 > 0) feed.begin_stage();
+        if constexpr (l1 > l0) tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i], feed.template load<l0>(cbuf));
+        else tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i]);
+        static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) { load_now(feed.template load<l0 + 1 + Lc>(cbuf)); });
+        if constexpr (l1 > l0 && l1 == NQ) feed.end_stage();
+        constexpr int lo = spread_lo(r, NR, T), hi = r < T ? spread_hi(r, NR, T) : lo;
+        static_for<hi - lo>([&](auto mc) {
+          constexpr int m = lo + mc;
+          if constexpr (m < NI) fa[h ^ 1][m] = read_a(m, rbuf, h ^ 1);
+          else fb[h ^ 1][m - NI] = read_b(m - NI, rbuf, h ^ 1);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (STAGED && h == 0) feed.put(nbuf);  // free since the barrier of the stage before
+    };
+    int s = 0;
+    do {
+      step(std::integral_constant<int, 0>{}, s);
+      step(std::integral_constant<int, 1>{}, s);
+    } while (++s < ns);
+    // No read of an accumulator may be scheduled before the wait states: all of them pass an empty asm after it.
     acc_hazard_guard();
 #pragma unroll
     for (int j = 0; j < WJ; ++j)
 #pragma unroll
       for (int i = 0; i < NI; ++i) asm volatile("" : "+a"(acc[j][i]));
+    // the stages past the end (zeros) have landed, and every wave is done reading: the buffers are free
+    if constexpr (!STAGED) wait_loads<0>();
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    barrier_keep_loads();
+    advance();
+
+    // ---- results
     // A lane's four results are neighbouring columns of one row: 8 or 16 bytes per store, straight from the
-    // accumulators.  The code is kept short on purpose: it runs once per tile, so it comes from L2, and with
-    // every address and rounding spelled out it took 28 us per tile.
+    // accumulators.  The code is kept short on purpose: with every address and rounding spelled out it took 28 us
+    // per tile, most of it waiting for instructions.
     const int rlane = wi * 16 + (lane & 15);  // row of fragment 0; the others follow 32 rows apart
     const int clane = WJ * wj * 16 + (lane >> 4) * 4;  // column of fragment 0; the others follow 16 apart
     const long long ldc = OP == kOpY ? a.ldy : OP == kOpDx ? a.ldx : a.ldw;
     const int ob = a.out_bf16 ? 2 : 4;
     char* out = (char*)(OP == kOpY ? a.y : OP == kOpDx ? a.x : a.w);
-    out += ((OP == kOpDw ? (size_t)t.e * a.w_stride + (size_t)t.i0 * ldc : (size_t)t.p0 * ldc) + t.j0) * ob;
+    out += ((OP == kOpDw ? ((size_t)t.part * a.E + t.e) * a.w_stride + (size_t)t.i0 * ldc : (size_t)t.p0 * ldc) + t.j0) * ob;
     const float* sw = TYPE == kI8 ? a.w_scale + (size_t)t.e * a.N + t.j0 : nullptr;
-    auto row_scale = [&](int i) {
+    float rs[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      rs[i] = 1.f;
       if constexpr (TYPE == kI8) {
         const int xr = x_row(a, t.p0 + min(32 * i + rlane, t.ni - 1));
-        return xr >= 0 ? a.x_scale[xr] : 0.f;
+        rs[i] = xr >= 0 ? a.x_scale[xr] : 0.f;
       }
-      return 1.f;
-    };
+    }
     // rows that start on a store's width and end on four columns
     if (((size_t)out | (size_t)(ldc * ob)) % (4 * ob) == 0 && t.nj % 4 == 0) {
       f32x4 cs[TYPE == kI8 ? WJ : 1];
@@ -555,12 +581,12 @@ struct TileKernel {
 #pragma unroll
           for (int r = 0; r < 4; ++r) cs[j][r] = sw[min(clane + 16 * j + r, t.nj - 1)];
       }
+      // the next tile's first stages have landed before the first store: its loop need not wait for stores
+      if constexpr (!STAGED) wait_loads<0>();
       auto rows = [&](auto bf) {
         constexpr bool BF = decltype(bf)::value;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          float rs = 1.f;
-          if constexpr (TYPE == kI8) rs = row_scale(i);
           if (32 * i + rlane >= t.ni) continue;
           char* p = out + ((size_t)(32 * i + rlane) * ldc + clane) * (BF ? 2 : 4);
 #pragma unroll
@@ -569,7 +595,7 @@ struct TileKernel {
             f32x4 v;
             if constexpr (TYPE == kI8) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = (float)acc[j][i][r] * rs * cs[j][r];
+              for (int r = 0; r < 4; ++r) v[r] = (float)acc[j][i][r] * rs[i] * cs[j][r];
             } else {
               v = acc[j][i];
             }
@@ -581,19 +607,18 @@ struct TileKernel {
       if (a.out_bf16) rows(std::true_type{});
       else rows(std::false_type{});
     } else {
-      // any other: 16 rows at a time through LDS (a region per wave; no wave reads operands any more), element by
-      // element
-      barrier_keep_loads();
-      float* reg = (float*)(lds + wave * (16 * 16 * WJ * 4));
+      // any other: 16 rows at a time through the wave's own LDS region, element by element
+      if constexpr (!STAGED) wait_loads<0>();
+      typedef __attribute__((address_space(3))) float* lfloat;
+      const lfloat reg = (lfloat)(lds + NB * STAGE + wave * REGION);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const float rs = row_scale(i);
 #pragma unroll
         for (int j = 0; j < WJ; ++j) {
           f32x4 v;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = TYPE == kI8 ? (float)acc[j][i][r] * rs : (float)acc[j][i][r];
-          *(f32x4*)(reg + (lane & 15) * 16 * WJ + 16 * j + (lane >> 4) * 4) = v;
+          for (int r = 0; r < 4; ++r) v[r] = TYPE == kI8 ? (float)acc[j][i][r] * rs[i] : (float)acc[j][i][r];
+          *(__attribute__((address_space(3))) f32x4*)(reg + (lane & 15) * 16 * WJ + 16 * j + (lane >> 4) * 4) = v;
         }
         store_rows(reg, out, ldc, t.ni - (32 * i + wi * 16), t.nj - WJ * wj * 16, 32 * i + wi * 16, WJ * wj * 16, 16 * WJ, sw,
                    a.out_bf16);
@@ -612,88 +637,124 @@ __device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, in
   row = band * kBand + r - col * h;
 }
 
-template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
-__global__ __launch_bounds__(256, (WI * WJ > 16 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
-  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED> Tk;
+// Each XCD's workgroups walk its range of tiles side by side (or take one tile each).
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
+__global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
   extern __shared__ __align__(1024) char smem[];
   const int nj = OP == kOpY ? a.N : a.K, ncol = (nj + Tk::BJ - 1) / Tk::BJ;
-  TileItem t;
-  int row, col;
-  const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
+  const int ntw = (a.N + Tk::BI - 1) / Tk::BI;  // row tiles of a weight gradient
+  GroupScan sc;
+  int total;  // (the launch checks that it fits)
   if constexpr (OP == kOpDw) {
-    const int nt = (a.N + Tk::BI - 1) / Tk::BI;
-    const int per = (int)((gridDim.x + kXcds - 1) / kXcds);  // the grid is a multiple of the XCDs
-    long long u = (long long)xcd * per + local;
-    const long long tiles = (long long)a.E * nt * ncol;
-    if (u >= tiles * a.split) return;
-    const int part = __builtin_amdgcn_readfirstlane((int)(u / tiles));
-    u -= part * tiles;
-    if (a.split > 1) a.w = (const char*)a.w + (size_t)part * a.E * a.w_stride * 4;
-    t.e = __builtin_amdgcn_readfirstlane((int)(u / ((long long)nt * ncol)));
-    band_order((int)(u - (long long)t.e * nt * ncol), nt, ncol, row, col);
-    const int2 g = group_range(a.offsets, t.e, a.rows);
-    t.p0 = g.x, t.nc = g.y;
-    if (a.split > 1) {  // this part of the group's rows, in whole stages
-      const int len = (g.y + a.split * Tk::KE - 1) / (a.split * Tk::KE) * Tk::KE;
-      const int from = min(part * len, g.y);
-      t.p0 += from, t.nc = min(len, g.y - from);
-    }
-    t.i0 = row * Tk::BI;
-    t.ni = min(Tk::BI, a.N - t.i0);
+    total = a.split * a.E * ntw * ncol;
   } else {
-    const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, Tk::BI);
-    const int total = sc.total * ncol, per = (total + kXcds - 1) / kXcds;
-    if (local >= per || xcd * per + local >= total) return;
-    const int u = xcd * per + local;
-    const GroupSpan g = sc.find(a.offsets, a.E, a.rows, Tk::BI, u / ncol);
-    t.e = g.e;
-    const int nt = (g.n + Tk::BI - 1) / Tk::BI;
-    band_order(u - g.first * ncol, nt, ncol, row, col);
-    const int r0 = (int)((long long)row * g.n / nt), r1 = (int)((long long)(row + 1) * g.n / nt);
-    t.p0 = g.p0 + r0, t.ni = r1 - r0, t.i0 = 0;
-    t.nc = OP == kOpY ? a.K : a.N;
+    sc = scan_groups(a.offsets, a.E, a.rows, Tk::BI);
+    total = sc.total * ncol;
   }
-  t.j0 = col * Tk::BJ;
-  t.nj = min(Tk::BJ, nj - t.j0);
-  // everything about the tile is uniform
-  t.i0 = __builtin_amdgcn_readfirstlane(t.i0), t.ni = __builtin_amdgcn_readfirstlane(t.ni);
-  t.j0 = __builtin_amdgcn_readfirstlane(t.j0), t.nj = __builtin_amdgcn_readfirstlane(t.nj);
-  t.p0 = __builtin_amdgcn_readfirstlane(t.p0), t.nc = __builtin_amdgcn_readfirstlane(t.nc);
-  if constexpr (OP == kOpDw) {
-    if (t.nc == 0) {  // an expert without rows
-      char* out = (char*)a.w + ((size_t)t.e * a.w_stride + (size_t)t.i0 * a.ldw + t.j0) * (a.out_bf16 ? 2 : 4);
+  const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
+  const int per = (int)(((long long)total + kXcds - 1) / kXcds), end = min(total, (xcd + 1) * per);
+  int u = xcd * per + blockIdx.x / kXcds;
+  auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+
+  // tile u, or the next one of this workgroup with anything to add up; false: none left
+  auto next_tile = [&](TileItem& t) __attribute__((always_inline)) {
+    for (; u < end; u += stride) {
+      int row, col;
+      t.part = 0;
+      if constexpr (OP == kOpDw) {
+        const int tiles = a.E * ntw * ncol;
+        t.part = uni(u / tiles);
+        const int v = u - t.part * tiles;
+        t.e = uni(v / (ntw * ncol));
+        band_order(v - t.e * ntw * ncol, ntw, ncol, row, col);
+        const int2 g = group_range(a.offsets, t.e, a.rows);
+        t.p0 = g.x, t.nc = g.y;
+        if (a.split > 1) {  // this part of the group's rows, in whole stages
+          const int len = (g.y + a.split * Tk::KE - 1) / (a.split * Tk::KE) * Tk::KE;
+          const int from = min(t.part * len, g.y);
+          t.p0 += from, t.nc = min(len, g.y - from);
+        }
+        t.i0 = row * Tk::BI;
+        t.ni = min(Tk::BI, a.N - t.i0);
+      } else {
+        const GroupSpan g = sc.find(a.offsets, a.E, a.rows, Tk::BI, u / ncol);
+        t.e = g.e;
+        const int nt = (g.n + Tk::BI - 1) / Tk::BI;
+        band_order(u - g.first * ncol, nt, ncol, row, col);
+        const int each = g.n / nt, longer = g.n - each * nt;  // the first `longer` tiles have one row more
+        t.p0 = g.p0 + row * each + min(row, longer), t.ni = each + (row < longer), t.i0 = 0;
+        t.nc = OP == kOpY ? a.K : a.N;
+      }
+      t.j0 = col * Tk::BJ;
+      t.nj = min(Tk::BJ, nj - t.j0);
+      // everything about the tile is uniform
+      t.i0 = uni(t.i0), t.ni = uni(t.ni), t.j0 = uni(t.j0), t.nj = uni(t.nj), t.p0 = uni(t.p0), t.nc = uni(t.nc);
+      if (OP != kOpDw || t.nc > 0) {
+        u += stride;
+        return true;
+      }
+      // an expert (or part) without rows
+      const size_t o = ((size_t)t.part * a.E + t.e) * a.w_stride + (size_t)t.i0 * a.ldw + t.j0;
       for (int i = threadIdx.x / 64; i < t.ni; i += kWaves)
-        for (int j = threadIdx.x % 64; j < t.nj; j += 64) store_out(out, (size_t)i * a.ldw + j, 0.f, a.out_bf16);
-      return;
+        for (int j = threadIdx.x % 64; j < t.nj; j += 64) store_out((void*)a.w, o + (size_t)i * a.ldw + j, 0.f, a.out_bf16);
     }
+    return false;
+  };
+
+  TileItem cur, next;
+  if (!next_tile(cur)) return;
+  typename Tk::Feed feed(a, (lptr)smem);
+  feed.init(cur);
+  if constexpr (!STAGED) feed.prologue();
+  bool more = false;
+  if constexpr (Tk::WALK) more = next_tile(next);
+  if constexpr (!STAGED) wait_loads<0>();
+  for (;;) {
+    TileItem after;
+    bool any_after = false;
+    auto advance = [&]() __attribute__((always_inline)) {
+      if (!Tk::WALK || !more) return;
+      feed.init(next);
+      if constexpr (!STAGED) feed.prologue();
+      any_after = next_tile(after);  // while the loads are under way
+    };
+    const int n = (cur.ni + 31) / 32;
+    static_for<WI>([&](auto ic) {
+      constexpr int NI = ic + 1;
+      if (n == NI) Tk::template body<NI>(a, cur, feed, advance);
+    });
+    if (!Tk::WALK || !more) break;
+    cur = next, next = after, more = any_after;
   }
-  const int n = (t.ni + 31) / 32;
-  static_for<WI>([&](auto ic) {
-    constexpr int NI = ic + 1;
-    if (n == NI) Tk::template body<NI>(a, t, (lptr)smem);
-  });
 }
 
-template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED>
+template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB = 2>
 int tile_launch_one(const GroupArgs& a, hipStream_t s) {
-  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED> Tk;
+  typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
   const int nj = OP == kOpY ? a.N : a.K;
   const long long nt = OP == kOpDw ? (long long)a.E * ((a.N + Tk::BI - 1) / Tk::BI) * a.split
                                    : group_tiles_max(a.rows, a.E, Tk::BI);
   long long nb = nt * ((nj + Tk::BJ - 1) / Tk::BJ);
   if (nb == 0) return MOE_OK;
-  nb = (nb + kXcds - 1) / kXcds * kXcds;
-  if (nb > kMaxThreads / 256) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
+  if (nb > 0x7FFFFF00LL) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles", nb);
   static bool attr_set[64];  // per device
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
   if (!attr_set[dev]) {
-    hipError_t e = hipFuncSetAttribute((const void*)grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED>,
+    hipError_t e = hipFuncSetAttribute((const void*)grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB>,
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)Tk::LDS);
     if (e != hipSuccess) return hip_fail(e, "moe_grouped_gemm: LDS attribute");
     attr_set[dev] = true;
   }
-  hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED>), dim3((unsigned)nb), dim3(256), Tk::LDS, s,
+  // a multiple of the XCDs, as many as are resident at a time (two per compute unit where LDS allows)
+  if (Tk::WALK) {
+    const long long slots = (long long)cu_count() * (2 * Tk::LDS <= 160 * 1024 ? 2 : 1) / kXcds * kXcds;
+    nb = std::min(nb, std::max(slots, (long long)kXcds));
+  }
+  nb = (nb + kXcds - 1) / kXcds * kXcds;
+  if (nb > kMaxThreads / 256) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
+  hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB>), dim3((unsigned)nb), dim3(256), Tk::LDS, s,
                      a);
   MOE_CHECK_LAUNCH("moe_grouped_gemm launch");
   return MOE_OK;

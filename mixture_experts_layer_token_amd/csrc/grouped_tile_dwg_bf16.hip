@@ -5,6 +5,7 @@ namespace moe {
 int launch_tile_dw_bf16_gather(const GroupArgs& a, TileShape t, hipStream_t s) {
   if (t == kStaged) return tile_launch_one<kOpDw, kBf16, 4, 4, true, true>(a, s);
   if (t == kSmall) return tile_launch_one<kOpDw, kBf16, 4, 4, true, false>(a, s);
+  if (t == kDeep) return tile_launch_one<kOpDw, kBf16, 4, 4, true, false, 4>(a, s);
   return tile_launch_one<kOpDw, kBf16, 8, 8, true, false>(a, s);
 }
 
