@@ -47,7 +47,8 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   if (op == kOpY) {
     // few rows and few tiles: the kernel that spreads each expert's features over N / 16 workgroups
     const long long groups = a.rows < a.E ? a.rows : a.E;
-    if ((a.rows + a.E - 1) / a.E <= 64 && groups * ((a.N + 127) / 128) < 512)
+    const long long avg = (a.rows + a.E - 1) / a.E, few = groups * ((a.N + 127) / 128);
+    if ((avg <= 32 && few < 512) || (avg <= 64 && few < 64))
       return launch_grouped_decode(a, type, t == kLarge, s);
   }
   if (op == kOpDw) {
@@ -67,11 +68,15 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     }
   }
   if (t == kLarge) {
-    // Tiles of 256 x 256 where they fill the machine, else of 128 x 128, two of which run on a compute unit at a time.
-    // Row counts are known on average only.
+    // Row counts are known on average only.  Tiles of 256 x 256 reuse their operands best, but one of them has a compute
+    // unit to itself: they need several rounds of tiles and rows to fill them.  Measured, 256 x 256 against 128 x 128:
+    // 8192 rows x 4096 x 4096 210 : 252 us (512 large tiles), 2048 rows 93 : 64 (128); 16384 rows over 16 experts of 1024 x 1024
+    // 66 : 51 (256 to 320); 4096 rows over 32 experts of 5760 x 2880 266 : 302, 2036 rows over 128 experts of 2880 x 2880
+    // 473 : 393.  The few tiles that leave compute units idle keep four stages in LDS instead of two: 1024 rows x 4096 x
+    // 4096 48 -> 39 us.
     const long long ni = op == kOpDw ? a.N : (a.rows + a.E - 1) / a.E, nj = op == kOpY ? a.N : a.K;
     auto tiles = [&](long long b) { return (long long)a.E * ((ni + b - 1) / b) * ((nj + b - 1) / b); };
-    if (tiles(256) < 256) t = tiles(128) <= 256 ? kDeep : kSmall;
+    if (tiles(256) < 448 || ni < 96) t = tiles(128) <= 256 ? kDeep : kSmall;
   }
   if (type == kF32) return launch_tile_f32(a, op, t, s);
   if (type == kI8) return launch_tile_y_i8(a, t, s);

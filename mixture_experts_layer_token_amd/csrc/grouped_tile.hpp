@@ -58,6 +58,20 @@ __device__ __forceinline__ void tile_mfma(f32x4& acc, const f32x4& b, const f32x
   asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+a"(acc) : "v"(b[E]), "v"(a[E]));
 }
 
+// The four values of an accumulator, read by assembly as well: the compiler then has no use of accumulators of its
+// own and never moves one (its copies next to an MFMA would miss the wait states, and do not fit beside 256 of
+// them).  Volatile: not before acc_hazard_guard().
+__device__ __forceinline__ float acc_get(const f32x4& acc, int r) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(acc[r]));
+  return v;
+}
+__device__ __forceinline__ float acc_get(const i32x4& acc, int r) {
+  int v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(acc[r]));
+  return (float)v;
+}
+
 typedef __attribute__((address_space(3))) char* lptr;
 constexpr int kStageC = 128;  // bytes of c per row and stage
 constexpr int kWaves = 4;
@@ -298,9 +312,6 @@ struct TileKernel {
   static constexpr bool IDX = GATHER && OP == kOpDw && !STAGED;  // x rows of c through perm_src
   static constexpr int RPL = IDX ? 1024 / (BJ * EB) : 1;  // c rows per load of B
   static constexpr int NX = IDX ? OpB::LQ * RPL : 1;
-  // A workgroup walks over several tiles, the next one's first loads under way while a tile's results are written; not
-  // with accumulators that fill the register file: the compiler then moves some of them around inside the loop.
-  static constexpr bool WALK = WI * WJ <= 16;
   static_assert(NB == 2 || (NB == 4 && !STAGED), "stages");
 
   // The operands of one tile on their way to LDS.
@@ -540,12 +551,7 @@ struct TileKernel {
       step(std::integral_constant<int, 0>{}, s);
       step(std::integral_constant<int, 1>{}, s);
     } while (++s < ns);
-    // No read of an accumulator may be scheduled before the wait states: all of them pass an empty asm after it.
     acc_hazard_guard();
-#pragma unroll
-    for (int j = 0; j < WJ; ++j)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) asm volatile("" : "+a"(acc[j][i]));
     // the stages past the end (zeros) have landed, and every wave is done reading: the buffers are free
     if constexpr (!STAGED) wait_loads<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);
@@ -593,11 +599,10 @@ struct TileKernel {
           for (int j = 0; j < WJ; ++j) {
             if (clane + 16 * j >= t.nj) continue;
             f32x4 v;
-            if constexpr (TYPE == kI8) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = (float)acc[j][i][r] * rs[i] * cs[j][r];
-            } else {
-              v = acc[j][i];
+            for (int r = 0; r < 4; ++r) {
+              v[r] = acc_get(acc[j][i], r);
+              if constexpr (TYPE == kI8) v[r] = v[r] * rs[i] * cs[j][r];
             }
             if constexpr (BF) *(u32x2*)(p + 32 * j) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             else *(f32x4*)(p + 64 * j) = v;
@@ -617,7 +622,7 @@ struct TileKernel {
         for (int j = 0; j < WJ; ++j) {
           f32x4 v;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = TYPE == kI8 ? (float)acc[j][i][r] * rs[i] : (float)acc[j][i][r];
+          for (int r = 0; r < 4; ++r) v[r] = acc_get(acc[j][i], r) * rs[i];
           *(__attribute__((address_space(3))) f32x4*)(reg + (lane & 15) * 16 * WJ + 16 * j + (lane >> 4) * 4) = v;
         }
         store_rows(reg, out, ldc, t.ni - (32 * i + wi * 16), t.nj - WJ * wj * 16, 32 * i + wi * 16, WJ * wj * 16, 16 * WJ, sw,
@@ -637,7 +642,7 @@ __device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, in
   row = band * kBand + r - col * h;
 }
 
-// Each XCD's workgroups walk its range of tiles side by side (or take one tile each).
+// Persistent: each XCD's workgroups walk its range of tiles side by side.
 template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
 __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
   typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
@@ -707,14 +712,13 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
   typename Tk::Feed feed(a, (lptr)smem);
   feed.init(cur);
   if constexpr (!STAGED) feed.prologue();
-  bool more = false;
-  if constexpr (Tk::WALK) more = next_tile(next);
+  bool more = next_tile(next);
   if constexpr (!STAGED) wait_loads<0>();
   for (;;) {
     TileItem after;
     bool any_after = false;
     auto advance = [&]() __attribute__((always_inline)) {
-      if (!Tk::WALK || !more) return;
+      if (!more) return;
       feed.init(next);
       if constexpr (!STAGED) feed.prologue();
       any_after = next_tile(after);  // while the loads are under way
@@ -724,7 +728,7 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
       constexpr int NI = ic + 1;
       if (n == NI) Tk::template body<NI>(a, cur, feed, advance);
     });
-    if (!Tk::WALK || !more) break;
+    if (!more) break;
     cur = next, next = after, more = any_after;
   }
 }
@@ -748,12 +752,8 @@ int tile_launch_one(const GroupArgs& a, hipStream_t s) {
     attr_set[dev] = true;
   }
   // a multiple of the XCDs, as many as are resident at a time (two per compute unit where LDS allows)
-  if (Tk::WALK) {
-    const long long slots = (long long)cu_count() * (2 * Tk::LDS <= 160 * 1024 ? 2 : 1) / kXcds * kXcds;
-    nb = std::min(nb, std::max(slots, (long long)kXcds));
-  }
-  nb = (nb + kXcds - 1) / kXcds * kXcds;
-  if (nb > kMaxThreads / 256) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
+  const long long slots = (long long)cu_count() * (2 * Tk::LDS <= 160 * 1024 ? 2 : 1) / kXcds * kXcds;
+  nb = (std::min(nb, std::max(slots, (long long)kXcds)) + kXcds - 1) / kXcds * kXcds;
   hipLaunchKernelGGL((grouped_tile_kernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB>), dim3((unsigned)nb), dim3(256), Tk::LDS, s,
                      a);
   MOE_CHECK_LAUNCH("moe_grouped_gemm launch");
