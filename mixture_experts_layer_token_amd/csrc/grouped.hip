@@ -37,6 +37,7 @@ size_t grouped_workspace(int, int rows, int N, int K, int E) {
 int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t s) {
   GroupArgs a = a0;
   a.split = 1;
+  a.each_xcd = 0;
   // direct loads: operand rows on 16-byte boundaries
   const int eb = type == kI8 ? 1 : type == kBf16 ? 2 : 4;
   auto al = [&](const void* p, long long ld) { return (uintptr_t)p % 16 == 0 && ld * eb % 16 == 0; };
@@ -67,6 +68,8 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
       return MOE_OK;
     }
   }
+  const long long ni = op == kOpDw ? a.N : (a.rows + a.E - 1) / a.E, nj = op == kOpY ? a.N : a.K;
+  auto tiles = [&](long long b) { return (long long)a.E * ((ni + b - 1) / b) * ((nj + b - 1) / b); };
   if (t == kLarge) {
     // Row counts are known on average only.  Tiles of 256 x 256 reuse their operands best, but one of them has a compute
     // unit to itself: they need several rounds of tiles and rows to fill them.  Measured, 256 x 256 against 128 x 128:
@@ -74,10 +77,12 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     // 66 : 51 (256 to 320); 4096 rows over 32 experts of 5760 x 2880 266 : 302, 2036 rows over 128 experts of 2880 x 2880
     // 473 : 393.  The few tiles that leave compute units idle keep four stages in LDS instead of two: 1024 rows x 4096 x
     // 4096 48 -> 39 us.
-    const long long ni = op == kOpDw ? a.N : (a.rows + a.E - 1) / a.E, nj = op == kOpY ? a.N : a.K;
-    auto tiles = [&](long long b) { return (long long)a.E * ((ni + b - 1) / b) * ((nj + b - 1) / b); };
     if (tiles(256) < 448 || ni < 96) t = tiles(128) <= 256 ? kDeep : kSmall;
   }
+  // Groups of many tiles are shared out over the XCDs one by one, as they may differ in cost (weight gradients of 8
+  // experts with 540 to 1000 rows 1228 -> 906 us); small ones stay on one XCD, whose L2 then holds their rows (16384 rows over 16
+  // experts of 1024 x 1024: 50 against 61 us).
+  a.each_xcd = tiles(t == kLarge ? 256 : 128) >= 128LL * a.E;
   if (type == kF32) return launch_tile_f32(a, op, t, s);
   if (type == kI8) return launch_tile_y_i8(a, t, s);
   return op == kOpY ? launch_tile_y_bf16(a, t, s) : op == kOpDx ? launch_tile_dx_bf16(a, t, s) : launch_tile_dw_bf16(a, t, s);

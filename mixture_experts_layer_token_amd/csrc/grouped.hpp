@@ -24,6 +24,7 @@ struct GroupArgs {
   // weights' gradient: parts each group's rows are cut into; with more than one, w is fp32 partial sums
   // [split][E][N][K]
   int split;
+  int each_xcd;  // tile kernel: every group's tiles are shared out over the XCDs (else a range of all tiles to each)
 };
 
 // Rows of expert e, clamped so that no offsets, however wrong, lead outside [0, rows).
@@ -46,16 +47,25 @@ inline long long group_tiles_max(int rows, int E, int mr) {
   return (long long)rows / mr + (rows < E ? rows : E);
 }
 
-// The groups' row tiles of mr rows in expert order.  Every wave scans the groups on its own (lane l takes experts
-// [l * per, (l + 1) * per)), so no LDS and no barrier is needed; totals and found tiles are uniform.
+// Tiles of a grouped product, shared out in `parts` (the XCDs, or 1: everything in one list).  A group of n rows has
+// ceil(n / mr) * ncol tiles, and part x takes a contiguous share of every group's, so that groups of unequal cost weigh
+// on all parts alike; the shares rotate from group to group.  A part's list is in group order.  Every wave scans the groups on its own (lane l takes groups [l * per, (l + 1) *
+// per)), so no LDS and no barrier is needed; totals and found tiles are uniform.
+__host__ __device__ __forceinline__ int2 part_range(int n, int e, int x, int parts) {  // {first, count} of the n tiles of group e
+  const int p = (x + e) % parts;
+  const int lo = (int)((long long)n * p / parts), hi = (int)((long long)n * (p + 1) / parts);
+  int2 r;
+  r.x = lo, r.y = hi - lo;
+  return r;
+}
 struct GroupSpan {
-  int e, p0, n, first;  // expert, its first grouped row, its rows, its first tile
+  int e, p0, n, tile;  // expert, its first grouped row, its rows, and which of its tiles
 };
 struct GroupScan {
-  int acc, incl, total;  // this lane's tiles are [acc, incl); total of all lanes
-  // the group that tile `slot` (< total) belongs to
-  __device__ __forceinline__ GroupSpan find(const int32_t* __restrict__ offsets, int E, int rows, int mr,
-                                            int slot) const {
+  int acc, incl, total;  // this lane's tiles are [acc, incl) of the part's list; its length
+  int mr, ncol, x, parts;
+  // tile `slot` (< total) of the list
+  __device__ __forceinline__ GroupSpan find(const int32_t* __restrict__ offsets, int E, int rows, int slot) const {
     const int per = (E + 63) / 64, lane = threadIdx.x & 63;
     GroupSpan f = {0, 0, 0, 0};
     const bool mine = slot >= acc && slot < incl;
@@ -63,30 +73,31 @@ struct GroupScan {
       int t = acc;
       for (int e = lane * per; e < min(E, (lane + 1) * per); ++e) {
         const int2 r = group_range(offsets, e, rows);
-        const int nt = (r.y + mr - 1) / mr;
-        if (slot >= t && slot < t + nt) f = GroupSpan{e, r.x, r.y, t};
-        t += nt;
+        const int2 p = part_range((r.y + mr - 1) / mr * ncol, e, x, parts);
+        if (slot >= t && slot < t + p.y) f = GroupSpan{e, r.x, r.y, p.x + slot - t};
+        t += p.y;
       }
     }
     const unsigned long long b = __ballot(mine);
     const int owner = b ? __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(b)) : 0;
     return GroupSpan{__builtin_amdgcn_readlane(f.e, owner), __builtin_amdgcn_readlane(f.p0, owner),
-                     __builtin_amdgcn_readlane(f.n, owner), __builtin_amdgcn_readlane(f.first, owner)};
+                     __builtin_amdgcn_readlane(f.n, owner), __builtin_amdgcn_readlane(f.tile, owner)};
   }
 };
-__device__ __forceinline__ GroupScan scan_groups(const int32_t* __restrict__ offsets, int E, int rows, int mr) {
+__device__ __forceinline__ GroupScan scan_groups(const int32_t* __restrict__ offsets, int E, int rows, int mr, int ncol,
+                                                 int x, int parts) {
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) / 64;
   int local = 0;
   for (int e = lane * per; e < min(E, (lane + 1) * per); ++e)
-    local += (group_range(offsets, e, rows).y + mr - 1) / mr;
+    local += part_range((group_range(offsets, e, rows).y + mr - 1) / mr * ncol, e, x, parts).y;
   int incl = local;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int t = __shfl_up(incl, off, 64);
     if (lane >= off) incl += t;
   }
-  return GroupScan{incl - local, incl, __builtin_amdgcn_readlane(incl, 63)};
+  return GroupScan{incl - local, incl, __builtin_amdgcn_readlane(incl, 63), mr, ncol, x, parts};
 }
 
 __device__ __forceinline__ void store_out(void* out, size_t i, float v, int bf16) {

@@ -136,11 +136,11 @@ template <int TYPE, bool DIRECT>
 __global__ __launch_bounds__(512) void grouped_decode_kernel(GroupArgs a) {
   __shared__ __align__(16) char smem[8 * 4 * 64 * 16];
   const int ncol = (a.N + kDecodeCols - 1) / kDecodeCols;
-  const int slot = blockIdx.x / ncol, col = blockIdx.x - slot * ncol;
-  const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, kDecodeRows);
-  if (slot >= sc.total) return;
-  const GroupSpan g = sc.find(a.offsets, a.E, a.rows, kDecodeRows, slot);
-  const int r0 = (slot - g.first) * kDecodeRows, rows = min(kDecodeRows, g.n - r0), mt = (rows + 15) / 16;
+  const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, kDecodeRows, ncol, 0, 1);
+  if ((int)blockIdx.x >= sc.total) return;
+  const GroupSpan g = sc.find(a.offsets, a.E, a.rows, blockIdx.x);
+  const int tile = g.tile / ncol, col = g.tile - tile * ncol;
+  const int r0 = tile * kDecodeRows, rows = min(kDecodeRows, g.n - r0), mt = (rows + 15) / 16;
   static_for<kDecodeRows / 16>([&](auto mc) {
     constexpr int MT = mc + 1;
     if (mt == MT) decode_body<TYPE, DIRECT, MT>(a, g.e, g.p0 + r0, rows, col * kDecodeCols, smem);

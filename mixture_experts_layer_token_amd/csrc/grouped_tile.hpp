@@ -632,9 +632,8 @@ struct TileKernel {
   }
 };
 
-// Tiles in launch order: workgroup b runs on XCD b % 8, and each XCD takes a contiguous range of the tiles, so
-// that its L2 serves the operands its workgroups share.  Tiles of an expert go in bands of up to 8 row tiles,
-// column by column: the 32 tiles an XCD works on at a time span 8 row and 4 column panels.
+// Workgroup b runs on XCD b % 8.  Tiles of an expert go in bands of up to 8 row tiles, column by column: the 32 tiles an
+// XCD works on at a time span few row and column panels.
 constexpr int kBand = 8;
 __device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, int& col) {
   const int band = u / (kBand * ncol), r = u - band * kBand * ncol, h = min(kBand, nt - band * kBand);
@@ -642,24 +641,36 @@ __device__ __forceinline__ void band_order(int u, int nt, int ncol, int& row, in
   row = band * kBand + r - col * h;
 }
 
-// Persistent: each XCD's workgroups walk its range of tiles side by side.
+// Persistent: each XCD's workgroups walk its tiles (part_range) side by side.
 template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
 __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
   typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
   extern __shared__ __align__(1024) char smem[];
   const int nj = OP == kOpY ? a.N : a.K, ncol = (nj + Tk::BJ - 1) / Tk::BJ;
   const int ntw = (a.N + Tk::BI - 1) / Tk::BI;  // row tiles of a weight gradient
-  GroupScan sc;
-  int total;  // (the launch checks that it fits)
-  if constexpr (OP == kOpDw) {
-    total = a.split * a.E * ntw * ncol;
-  } else {
-    sc = scan_groups(a.offsets, a.E, a.rows, Tk::BI);
-    total = sc.total * ncol;
-  }
   const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
-  const int per = (int)(((long long)total + kXcds - 1) / kXcds), end = min(total, (xcd + 1) * per);
-  int u = xcd * per + blockIdx.x / kXcds;
+  // This XCD's tiles: its part of every group, or (few tiles per group) a contiguous range of all of them
+  const int parts = a.each_xcd ? kXcds : 1, px = a.each_xcd ? xcd : 0;
+  GroupScan sc;
+  int end;
+  if constexpr (OP == kOpDw) {
+    const int n = a.split * a.E;  // parts of groups, all of ntw * ncol tiles: each 8 of them give an XCD that many
+    if (a.each_xcd) {
+      end = n / kXcds * ntw * ncol;
+      for (int e = n / kXcds * kXcds; e < n; ++e) end += part_range(ntw * ncol, e, xcd, kXcds).y;
+    } else {
+      end = n * ntw * ncol;
+    }
+  } else {
+    sc = scan_groups(a.offsets, a.E, a.rows, Tk::BI, ncol, px, parts);
+    end = sc.total;
+  }
+  int u = blockIdx.x / kXcds;
+  if (!a.each_xcd) {
+    const int2 r = part_range(end, 0, xcd, kXcds);
+    u += r.x;
+    end = r.x + r.y;
+  }
   auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
 
   // tile u, or the next one of this workgroup with anything to add up; false: none left
@@ -668,11 +679,16 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
       int row, col;
       t.part = 0;
       if constexpr (OP == kOpDw) {
-        const int tiles = a.E * ntw * ncol;
-        t.part = uni(u / tiles);
-        const int v = u - t.part * tiles;
-        t.e = uni(v / (ntw * ncol));
-        band_order(v - t.e * ntw * ncol, ntw, ncol, row, col);
+        const int tiles = ntw * ncol;
+        int e = u / tiles * parts, v = u % tiles;
+        int2 p = part_range(tiles, e, px, parts);
+        while (v >= p.y) {
+          v -= p.y;
+          p = part_range(tiles, ++e, px, parts);
+        }
+        t.part = uni(e / a.E);
+        t.e = uni(e - t.part * a.E);
+        band_order(uni(p.x + v), ntw, ncol, row, col);
         const int2 g = group_range(a.offsets, t.e, a.rows);
         t.p0 = g.x, t.nc = g.y;
         if (a.split > 1) {  // this part of the group's rows, in whole stages
@@ -683,10 +699,11 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
         t.i0 = row * Tk::BI;
         t.ni = min(Tk::BI, a.N - t.i0);
       } else {
-        const GroupSpan g = sc.find(a.offsets, a.E, a.rows, Tk::BI, u / ncol);
+        const GroupSpan g = sc.find(a.offsets, a.E, a.rows, u);
+        if (g.n <= 0) return false;  // (only groups that overlap, more tiles than an int counts, can lead here)
         t.e = g.e;
         const int nt = (g.n + Tk::BI - 1) / Tk::BI;
-        band_order(u - g.first * ncol, nt, ncol, row, col);
+        band_order(g.tile, nt, ncol, row, col);
         const int each = g.n / nt, longer = g.n - each * nt;  // the first `longer` tiles have one row more
         t.p0 = g.p0 + row * each + min(row, longer), t.ni = each + (row < longer), t.i0 = 0;
         t.nc = OP == kOpY ? a.K : a.N;
