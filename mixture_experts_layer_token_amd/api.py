@@ -203,32 +203,45 @@ def moe_grouped_workspace(dt, rows, N, K, E) -> int:
     return int(lib().moe_grouped_workspace(DT[dt], rows, N, K, E))
 
 
+def _ptr(t):
+    """Address of a contiguous device tensor (None -> NULL)."""
+    if t is None:
+        return None
+    assert t.is_cuda and t.is_contiguous(), "expected a contiguous device tensor"
+    return t.data_ptr()
+
+
 def _rowp(t):
-    """Device pointer of a tensor whose last dimension is contiguous (rows may be strided)."""
+    """Address of a device tensor whose last dimension is contiguous (rows may be strided)."""
     assert t.is_cuda and (t.shape[-1] <= 1 or t.stride(-1) == 1), "expected a device tensor with contiguous rows"
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _step(t, dim):
     """Elements between neighbours along `dim` (0, the default of the C call, where there is only one)."""
     if t.shape[dim] <= 1:
         return 0
-    if t.stride(dim) < 1:
+    step = t.stride(dim)
+    if step < 1:
         raise ValueError("a tensor expanded along a dimension has no rows of its own")
-    return t.stride(dim)
+    return step
 
 
 def _launch(f, args, tensors, stream):
     """Call f(*args, stream) on the device that holds the tensors, whichever is current."""
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors on %s and %s" % (dev, t.device))
-    if dev.index == torch.cuda.current_device():
-        check(f(*args, _stream(stream)))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on devices %d and %d" % (dev, t.get_device()))
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = torch._C._cuda_getCurrentRawStream(dev)  # (torch.cuda.current_stream costs more than the rest of a call)
+    if dev == torch.cuda.current_device():
+        check(f(*args, s))
     else:
         with torch.cuda.device(dev):
-            check(f(*args, _stream(stream)))
+            check(f(*args, s))
 
 
 def _grouped(x, w, y, offsets, perm_src, k) -> MoeGrouped:
@@ -244,13 +257,8 @@ def _grouped(x, w, y, offsets, perm_src, k) -> MoeGrouped:
             raise ValueError("x has %d rows, y %d (pass perm_src to gather)" % (x.shape[0], rows))
     elif perm_src.dtype != torch.int32 or perm_src.numel() < rows:
         raise ValueError("perm_src: %d int32 entries expected" % rows)
-    g = MoeGrouped()
-    g.rows, g.E, g.N, g.K = rows, E, N, K
-    g.offsets = _dp(offsets).value
-    g.perm_src = None if perm_src is None else _dp(perm_src).value
-    g.k, g.x_rows = k, x.shape[0]
-    g.ldx, g.ldy, g.ldw, g.w_stride = _step(x, 0), _step(y, 0), _step(w, 1), _step(w, 0)
-    return g
+    return MoeGrouped(rows, E, N, K, _ptr(offsets), _ptr(perm_src), k, x.shape[0], _step(x, 0), _step(y, 0), _step(w, 1),
+                      _step(w, 0))
 
 
 def _same_dt(a, b):
@@ -263,7 +271,7 @@ def _grouped_ws(ws, dt, g, device):
     if ws is None:
         need = int(lib().moe_grouped_workspace(dt, g.rows, g.N, g.K, g.E))
         ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    return ws, _dp(ws), 0 if ws is None else ws.numel() * ws.element_size()
+    return ws, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def moe_grouped_gemm(x, w, offsets, y, perm_src=None, k=1, ws=None, stream=None):
@@ -300,7 +308,7 @@ def _need(t, dtype, shape, what):
 def _n_rows(n):
     if n is not None and (n.dtype != torch.int32 or n.numel() != 1):
         raise ValueError("n_rows: one int32 on the device expected")
-    return _dp(n)
+    return _ptr(n)
 
 
 def moe_quant_rows(x, q, scale, act="none", n_rows=None, stream=None):
@@ -310,7 +318,7 @@ def moe_quant_rows(x, q, scale, act="none", n_rows=None, stream=None):
     _need(x, x.dtype, (rows, 2 * K if act == "swiglu" else K), "x")
     _need(q, torch.int8, (rows, K), "q")
     _need(scale, torch.float32, (rows,), "scale")
-    _launch(lib().moe_quant_rows, (_dp(x), _dt(x), rows, K, ACT[act], _n_rows(n_rows), _dp(q), _dp(scale)),
+    _launch(lib().moe_quant_rows, (_ptr(x), _dt(x), rows, K, ACT[act], _n_rows(n_rows), _ptr(q), _ptr(scale)),
             (x, q, scale, n_rows), stream)
 
 
@@ -322,7 +330,7 @@ def moe_grouped_gemm_i8(q, q_scale, w, w_scale, offsets, y, perm_src=None, k=1, 
     _need(q_scale, torch.float32, (q.shape[0],), "q_scale")
     _need(w_scale, torch.float32, (g.E, g.N), "w_scale")
     _launch(lib().moe_grouped_gemm_i8,
-            (ctypes.byref(g), _rowp(q), _dp(q_scale), _rowp(w), _dp(w_scale), _rowp(y), _dt(y)),
+            (ctypes.byref(g), _rowp(q), _ptr(q_scale), _rowp(w), _ptr(w_scale), _rowp(y), _dt(y)),
             (q, q_scale, w, w_scale, y, offsets, perm_src), stream)
 
 
@@ -330,7 +338,7 @@ def moe_swiglu(gu, h, n_rows=None, stream=None):
     """h = SiLU(g) * u for rows gu = [g | u]."""
     rows, I = h.shape
     _need(gu, h.dtype, (rows, 2 * I), "gu")
-    _launch(lib().moe_swiglu, (_dp(gu), _dt(gu), rows, I, _n_rows(n_rows), _dp(h)), (gu, h, n_rows), stream)
+    _launch(lib().moe_swiglu, (_ptr(gu), _dt(gu), rows, I, _n_rows(n_rows), _ptr(h)), (gu, h, n_rows), stream)
 
 
 def moe_swiglu_grad(gu, dh, dgu, h=None, n_rows=None, stream=None):
@@ -340,7 +348,7 @@ def moe_swiglu_grad(gu, dh, dgu, h=None, n_rows=None, stream=None):
     _need(dgu, dh.dtype, (rows, 2 * I), "dgu")
     if h is not None:
         _need(h, dh.dtype, (rows, I), "h")
-    _launch(lib().moe_swiglu_grad, (_dp(gu), _dp(dh), _dt(gu), rows, I, _n_rows(n_rows), _dp(dgu), _dp(h)),
+    _launch(lib().moe_swiglu_grad, (_ptr(gu), _ptr(dh), _dt(gu), rows, I, _n_rows(n_rows), _ptr(dgu), _ptr(h)),
             (gu, dh, dgu, h, n_rows), stream)
 
 
@@ -367,8 +375,8 @@ def moe_combine_grad(dout, y_perm, topk_w, inv_perm, k, dy_perm, dtopk_w, topk_i
         if topk_ids is not None:
             _need(topk_ids, torch.int32, (T, k), "topk_ids")
     _launch(lib().moe_combine_grad,
-            (_dp(dout), _dt(dout), _dp(y_perm), _dp(topk_w), _dp(inv_perm), T, k, H, _dp(dy_perm), _dt(dy_perm),
-             _dp(dtopk_w), _dp(topk_ids), E, _dp(dlogits)),
+            (_ptr(dout), _dt(dout), _ptr(y_perm), _ptr(topk_w), _ptr(inv_perm), T, k, H, _ptr(dy_perm), _dt(dy_perm),
+             _ptr(dtopk_w), _ptr(topk_ids), E, _ptr(dlogits)),
             (dout, y_perm, topk_w, inv_perm, dy_perm, dtopk_w, topk_ids, dlogits), stream)
 
 

@@ -1,0 +1,70 @@
+"""A routed-expert MoE layer with 8-bit integer experts (W8A8): int8 weights with a scale per output channel, and
+activations quantized on the way with a scale per token.
+
+The experts take half the bytes of bf16 ones.  Forward: moe_route_permute on the bf16 (or fp32) tokens, moe_quant_rows
+(each token once, before it is gathered), moe_grouped_gemm_i8 (gate/up), moe_quant_rows with the SwiGLU gate (the
+gated rows exist in 8 bits only), moe_grouped_gemm_i8 (down, fp32 results), moe_combine.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import api
+
+
+def quantize_weights(w: torch.Tensor):
+    """[E, N, K] bf16 / fp32 -> (int8 [E, N, K], scale [E, N]): one scale per output channel."""
+    E, N, K = w.shape
+    q = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
+    s = torch.empty((E, N), dtype=torch.float32, device=w.device)
+    api.moe_quant_rows(w.contiguous().view(E * N, K), q.view(E * N, K), s.view(E * N))
+    return q, s
+
+
+class MoeInt8Layer:
+    """`w_gate_up` [E, 2I, H] (gate rows, then up rows) and `w_down` [E, H, I] are quantized here; the router stays in
+    its own type.  All buffers are allocated once for batches of up to max_T tokens."""
+
+    def __init__(self, w_router, bias, w_gate_up, w_down, k, max_T=1):
+        self.w_router, self.bias, self.k = w_router, bias, k
+        self.E, self.H, self.I = w_gate_up.shape[0], w_gate_up.shape[2], w_down.shape[2]
+        if tuple(w_gate_up.shape) != (self.E, 2 * self.I, self.H) or tuple(w_down.shape) != (self.E, self.H, self.I):
+            raise ValueError("w_gate_up %s and w_down %s do not fit" % (tuple(w_gate_up.shape), tuple(w_down.shape)))
+        self.gate_up = quantize_weights(w_gate_up)
+        self.down = quantize_weights(w_down)
+        self._alloc(max_T)
+
+    def _alloc(self, T):
+        d, k, H, I, E = self.w_router.device, self.k, self.H, self.I, self.E
+        self.max_T, n = T, max(T * k, 1)
+        i32, f32 = dict(dtype=torch.int32, device=d), dict(dtype=torch.float32, device=d)
+        self.ids, self.gates = torch.empty((T, k), **i32), torch.empty((T, k), **f32)
+        self.counts, self.offsets = torch.empty(E, **i32), torch.empty(E + 1, **i32)
+        self.perm, self.inv = torch.empty(n, **i32), torch.empty(n, **i32)
+        self.q, self.q_scale = torch.empty((T, H), dtype=torch.int8, device=d), torch.empty(T, **f32)
+        self.gu = torch.empty((n, 2 * I), dtype=torch.bfloat16, device=d)
+        self.h, self.h_scale = torch.empty((n, I), dtype=torch.int8, device=d), torch.empty(n, **f32)
+        self.y = torch.empty((n, H), **f32)
+        xdt = "f32" if self.w_router.dtype == torch.float32 else "bf16"
+        rws = max(api.moe_route_permute_workspace(t, H, E, k, xdt) for t in range(1, T + 1))
+        self.rws = torch.empty(max(rws, 256), dtype=torch.uint8, device=d)
+
+    def forward(self, x, out=None):
+        """One layer forward on the current stream (x [T, H] in the router's type)."""
+        T, k = x.shape[0], self.k
+        if T > self.max_T:
+            self._alloc(T)
+        if out is None:
+            out = torch.empty_like(x)
+        if T == 0:
+            return out
+        n = T * k
+        ids, gates, perm, inv = self.ids[:T], self.gates[:T], self.perm[:n], self.inv[:n]
+        api.moe_route_permute(x, self.w_router, self.bias, k, ids, gates, self.counts, self.offsets, perm, inv,
+                              ws=self.rws)
+        api.moe_quant_rows(x, self.q[:T], self.q_scale[:T])
+        api.moe_grouped_gemm_i8(self.q[:T], self.q_scale[:T], *self.gate_up, self.offsets, self.gu[:n], perm_src=perm, k=k)
+        api.moe_quant_rows(self.gu[:n], self.h[:n], self.h_scale[:n], act="swiglu", n_rows=self.offsets[-1:])
+        api.moe_grouped_gemm_i8(self.h[:n], self.h_scale[:n], *self.down, self.offsets, self.y[:n])
+        api.moe_combine(self.y[:n], gates, inv, k, None, out)
+        return out

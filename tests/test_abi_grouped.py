@@ -93,12 +93,9 @@ def test_workspace():
 
 
 def test_too_many_tiles():
-    g = desc(rows=1 << 24, N=1 << 20, K=1 << 20, E=1)
-    need = [L.moe_grouped_workspace(BF16, g.rows, g.N, g.K, g.E)][0]
-    rc = calls(g, ws=P if need else None, n=need)
-    assert rc[0] == UNSUPPORTED and rc[1] == UNSUPPORTED
     g = desc(rows=1, N=1 << 20, K=1 << 20, E=1024)
     assert calls(g, ws=P, n=1 << 62)[2] == UNSUPPORTED
+    assert b"tiles" in L.moe_last_error()
 
 
 def test_quant_and_gate_refusals():
