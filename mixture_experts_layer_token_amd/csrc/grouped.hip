@@ -1,4 +1,7 @@
 // Products grouped by expert over plain weights: choice of the kernel, and the sum of split weight gradients.
+#include <algorithm>
+#include <cmath>
+
 #include "grouped.hpp"
 
 namespace moe {
@@ -27,6 +30,24 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   store_out(dw, (size_t)(e * w_stride + (row - e * N) * ldw + (i - row * K)), v, bf16);
 }
 
+// The tile shape that takes the least time, from rounds of tiles and stages of 128 bytes (us; fitted to measured calls).
+// A 256 x 256 tile has a compute unit to itself: 1.46 per stage of full tiles, 10 to begin and end; 128 x 128 ones go two
+// to a compute unit, 0.94 and 7; where they leave units idle anyway, four stages in LDS instead of two hide the loads
+// better: 0.5 and 8.  Rows that do not fill a tile save matrix instructions but not loads.  Measured, large against small:
+// 8192 rows x 4096 x 4096 210 : 252 us, 2048 rows 93 : 64; 16384 rows over 16 experts of 1024 x 1024 66 : 50; 16384 rows over
+// 32 experts of 5760 x 2880 594 : 681, 4096 rows 264 : 302, 2036 rows over 128 experts of 2880 x 2880 473 : 393; weight gradient of 8192 rows, 4096 x
+// 4096, 197 : 250.  Small against deep: 1024 rows x 4096 x 4096 48 : 38.
+TileShape cheapest_shape(const GroupArgs& a, int op, int eb, double large, double small, double rows) {
+  const double c = op == kOpY ? a.K : op == kOpDx ? a.N : (double)a.rows / a.E;
+  const double ns = std::max(1.0, std::ceil(c * eb / 128));
+  const double fl = std::max(0.6, rows / 256), fs = std::max(0.6, std::min(1.0, rows / 128));
+  const double cus = cu_count();
+  const double cost_large = std::ceil(large / cus) * (1.46 * fl * ns + 10);
+  const double cost_small = std::ceil(small / (2 * cus)) * (0.94 * fs * ns + 7);
+  const double cost_deep = small <= cus ? 0.5 * fs * ns + 8 : 1e30;
+  return cost_large <= std::min(cost_small, cost_deep) ? kLarge : cost_deep < cost_small ? kDeep : kSmall;
+}
+
 }  // namespace
 
 size_t grouped_workspace(int, int rows, int N, int K, int E) {
@@ -48,8 +69,8 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   if (op == kOpY) {
     // few rows and few tiles: the kernel that spreads each expert's features over N / 16 workgroups
     const long long groups = a.rows < a.E ? a.rows : a.E;
-    const long long avg = (a.rows + a.E - 1) / a.E, few = groups * ((a.N + 127) / 128);
-    if ((avg <= 32 && few < 512) || (avg <= 64 && few < 64))
+    const long long mean = (a.rows + a.E - 1) / a.E, few = groups * ((a.N + 127) / 128);
+    if ((mean <= 32 && few < 512) || (mean <= 64 && few < 64))
       return launch_grouped_decode(a, type, t == kLarge, s);
   }
   if (op == kOpDw) {
@@ -68,21 +89,18 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
       return MOE_OK;
     }
   }
-  const long long ni = op == kOpDw ? a.N : (a.rows + a.E - 1) / a.E, nj = op == kOpY ? a.N : a.K;
-  auto tiles = [&](long long b) { return (long long)a.E * ((ni + b - 1) / b) * ((nj + b - 1) / b); };
-  if (t == kLarge) {
-    // Row counts are known on average only.  Tiles of 256 x 256 reuse their operands best, but one of them has a compute
-    // unit to itself: they need several rounds of tiles and rows to fill them.  Measured, 256 x 256 against 128 x 128:
-    // 8192 rows x 4096 x 4096 210 : 252 us (512 large tiles), 2048 rows 93 : 64 (128); 16384 rows over 16 experts of 1024 x 1024
-    // 66 : 51 (256 to 320); 4096 rows over 32 experts of 5760 x 2880 266 : 302, 2036 rows over 128 experts of 2880 x 2880
-    // 473 : 393.  The few tiles that leave compute units idle keep four stages in LDS instead of two: 1024 rows x 4096 x
-    // 4096 48 -> 39 us.
-    if (tiles(256) < 448 || ni < 96) t = tiles(128) <= 256 ? kDeep : kSmall;
-  }
+  // tiles of b x b (row counts are known on average only: half a tile more per group)
+  const double avg = (double)a.rows / a.E;
+  const long long nj = op == kOpY ? a.N : a.K;
+  auto tiles = [&](int b) {
+    const double ni = op == kOpDw ? (double)((a.N + b - 1) / b) : a.E == 1 ? (double)((a.rows + b - 1) / b) : std::max(1.0, avg / b + 0.5);
+    return ni * a.E * ((nj + b - 1) / b);
+  };
+  if (t == kLarge) t = cheapest_shape(a, op, eb, tiles(256), tiles(128), op == kOpDw ? 256 : std::min(avg, 256.0));
   // Groups of many tiles are shared out over the XCDs one by one, as they may differ in cost (weight gradients of 8
   // experts with 540 to 1000 rows 1228 -> 906 us); small ones stay on one XCD, whose L2 then holds their rows (16384 rows over 16
   // experts of 1024 x 1024: 50 against 61 us).
-  a.each_xcd = tiles(t == kLarge ? 256 : 128) >= 128LL * a.E;
+  a.each_xcd = tiles(t == kLarge ? 256 : 128) >= 128.0 * a.E;
   if (type == kF32) return launch_tile_f32(a, op, t, s);
   if (type == kI8) return launch_tile_y_i8(a, t, s);
   return op == kOpY ? launch_tile_y_bf16(a, t, s) : op == kOpDx ? launch_tile_dx_bf16(a, t, s) : launch_tile_dw_bf16(a, t, s);

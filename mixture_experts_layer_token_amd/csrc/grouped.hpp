@@ -16,6 +16,7 @@ struct GroupArgs {
   const int32_t* offsets;
   const int32_t* perm_src;  // or null: x rows are grouped rows
   int k, x_rows;            // x row of grouped row p: perm_src[p] / k, a row of zeros unless in [0, x_rows)
+  unsigned k_inv;           // ceil(2^32 / k)
   int rows, E, N, K;
   long long ldx, ldy, ldw, w_stride;  // elements
   const float* x_scale;  // 8-bit operands: scale of every x row and of every w row ([E][N])
@@ -33,13 +34,18 @@ __device__ __forceinline__ int2 group_range(const int32_t* __restrict__ offsets,
   return make_int2(lo, max(hi - lo, 0));
 }
 
-// x row of grouped row p (p < rows), or -1 where perm_src names none
-__device__ __forceinline__ int x_row(const GroupArgs& a, int p) {
-  if (!a.perm_src) return p;
-  const int s = a.perm_src[p];
-  const int r = s / a.k;
+// s / k for the flat index of a pair, s < x_rows * k <= 2^28: the product with ceil(2^32 / k) is off by less than 2^-4 <= 1 / k
+// there.  (Of larger s, which names no row, only "at least x_rows" is needed, and the product keeps that.)
+__device__ __forceinline__ int div_k(const GroupArgs& a, int s) {
+  return a.k == 1 ? s : (int)__umulhi((unsigned)s, a.k_inv);
+}
+// x row that an entry of perm_src names, or -1 for none
+__device__ __forceinline__ int named_row(const GroupArgs& a, int s) {
+  const int r = div_k(a, s);
   return s >= 0 && r < a.x_rows ? r : -1;
 }
+// x row of grouped row p (p < rows), or -1
+__device__ __forceinline__ int x_row(const GroupArgs& a, int p) { return a.perm_src ? named_row(a, a.perm_src[p]) : p; }
 
 // Row tiles of mr rows over the groups in expert order; at most this many exist for any offsets whose
 // groups do not overlap (launch bound: overlapping groups are cut off there).

@@ -36,6 +36,7 @@ GroupArgs group_args(const moe_grouped* g, const void* x, const void* w, const v
   a.x = x, a.w = w, a.y = y;
   a.offsets = g->offsets, a.perm_src = g->perm_src;
   a.k = g->perm_src ? g->k : 1;
+  a.k_inv = a.k > 1 ? (unsigned)((0x100000000ULL + a.k - 1) / a.k) : 0;
   a.x_rows = g->perm_src ? g->x_rows : g->rows;
   a.rows = g->rows, a.E = g->E, a.N = g->N, a.K = g->K;
   a.ldx = g->ldx ? g->ldx : g->K;

@@ -130,14 +130,14 @@ struct Contig {
   int c_byte;         // its byte of c within a stage
   gptr row[LQ];       // (fetch) its rows; null: zeros
 
-  // off(r): byte offset of row r from p, or kOutside for a row of zeros; all < bytes
+  // off(r, q): byte offset of row r (load q) from p, or kOutside for a row of zeros; all < bytes
   template <typename F>
   __device__ __forceinline__ void init(int wave, int lane, gptr p, unsigned bytes, int c_bytes, F&& off) {
     base = p, span = bytes, left = c_bytes;
     c_byte = ((lane & 7) ^ (lane >> 3)) * 16;  // 8 rows per load: chunk c of row r goes to slot c ^ (r & 7)
 #pragma unroll
     for (int q = 0; q < LQ; ++q) {
-      const unsigned o = off((q * kWaves + wave) * 8 + lane / 8);
+      const unsigned o = off((q * kWaves + wave) * 8 + lane / 8, q);
       voff[q] = o == kOutside ? o : o + c_byte;
     }
   }
@@ -290,10 +290,6 @@ struct TileItem {
   int part;                       // weights' gradient: part of the group's rows
 };
 
-// Division of a grouped pair's flat index by k (2 <= k <= 16, index below 2^28): multiplication by ceil(2^32 / k),
-// off by less than 1 / k there.
-__device__ __forceinline__ int div_k(int s, int k, unsigned magic) { return k == 1 ? s : (int)__umulhi((unsigned)s, magic); }
-
 // STAGED: operands pass through registers (any alignment, stride and extent).  NB: stages in LDS.
 template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
 struct TileKernel {
@@ -319,7 +315,6 @@ struct TileKernel {
     const GroupArgs& a;
     const int lane, wave;
     const lptr lds;
-    const unsigned magic;
     TileItem t;
     OpA A;
     OpB B;
@@ -327,14 +322,27 @@ struct TileKernel {
     // they name for the stage to be loaded next (kOutside: zeros)
     int idx_next[NX];
     unsigned idx[NX], bcol[OpB::LQ];
+    // offsets of the gathered x rows of the tile to come
+    static constexpr bool AHEAD = OP == kOpY && !STAGED;
+    unsigned ahead[AHEAD ? OpA::LQ : 1];
     // STAGED: a stage in registers
     u32x4 held[STAGED ? NL : 1];
     int fetched;  // stages
 
     __device__ __forceinline__ Feed(const GroupArgs& args, lptr smem)
-        : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lds(smem),
-          magic(args.k > 1 ? (unsigned)((0x100000000ULL + args.k - 1) / args.k) : 0) {}
+        : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lds(smem) {}
 
+    // looks up what init(item) needs from memory
+    __device__ __forceinline__ void look_ahead(const TileItem& item) {
+      if constexpr (AHEAD) {
+        if (!a.perm_src) return;
+#pragma unroll
+        for (int q = 0; q < OpA::LQ; ++q) {
+          const int xr = x_row(a, item.p0 + min((q * kWaves + wave) * 8 + lane / 8, item.ni - 1));
+          ahead[q] = xr >= 0 ? (unsigned)xr * (unsigned)a.ldx * EB : kOutside;
+        }
+      }
+    }
     __device__ __forceinline__ void init(const TileItem& item) {
       t = item;
       const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
@@ -357,19 +365,17 @@ struct TileKernel {
       } else if constexpr (OP == kOpY) {
         const unsigned cb = (unsigned)a.K * EB;
         if (a.perm_src)
-          A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb, [&](int r) -> unsigned {
-            const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
-            return xr >= 0 ? (unsigned)xr * ldx : kOutside;
-          });
+          A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb,
+                 [&](int, int q) -> unsigned { return ahead[AHEAD ? q : 0]; });
         else
           A.init(wave, lane, x + (size_t)t.p0 * a.ldx * EB, (unsigned)(t.ni - 1) * ldx + cb, cb,
-                 [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
+                 [&](int r, int) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
         B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1) * ldw + cb, cb,
-               [&](int r) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
+               [&](int r, int) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
       } else if constexpr (OP == kOpDx) {
         const unsigned cb = (unsigned)a.N * EB;
         A.init(wave, lane, y + (size_t)t.p0 * a.ldy * EB, (unsigned)(t.ni - 1) * ldy + cb, cb,
-               [&](int r) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
+               [&](int r, int) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
         B.init(wave, lane, w + (size_t)t.j0 * EB, ldw, t.nc, t.nj * EB);
       } else {
         A.init(wave, lane, y + ((size_t)t.p0 * a.ldy + t.i0) * EB, ldy, t.nc, t.ni * EB);
@@ -391,7 +397,7 @@ struct TileKernel {
       if constexpr (IDX) {
 #pragma unroll
         for (int n = 0; n < NX; ++n) {
-          const int v = idx_next[n], r = div_k(v, a.k, magic);
+          const int v = idx_next[n], r = div_k(a, v);
           const bool ok = v >= 0 && r < a.x_rows && s * KE + (n / RPL * kWaves + wave) * RPL + n % RPL < t.nc;
           idx[n] = ok ? (unsigned)r * (unsigned)a.ldx * EB : kOutside;
         }
@@ -525,12 +531,12 @@ struct TileKernel {
       }
       __builtin_amdgcn_sched_barrier(0);
       const int cbuf = s & (NB - 1), nbuf = (s + 1) & (NB - 1), rbuf = h == 0 ? cbuf : nbuf;
-      // slots: reads over the first three quarters of the MFMAs, loads over the first half
+      // slots: reads over the first three quarters of the MFMAs, loads over all of them (over half: 2% slower)
       constexpr int R = WJ * NI * TT::MPF, NR = NI + WJ, T = 3 * R / 4 > 0 ? 3 * R / 4 : 1;
-      constexpr int NQ = h == 1 && !STAGED ? NL : 0, TL = R / 2 > 0 ? R / 2 : 1;
+      constexpr int NQ = h == 1 && !STAGED ? NL : 0;
       static_for<R>([&](auto rc) {
         constexpr int r = rc, e = r / (WJ * NI), j = r % (WJ * NI) / NI, i = r % NI;
-        constexpr int l0 = spread_lo(r, NQ, TL), l1 = r < TL ? spread_hi(r, NQ, TL) : l0;
+        constexpr int l0 = spread_lo(r, NQ, R), l1 = spread_hi(r, NQ, R);
         if constexpr (l0 == 0 && l1 > 0) feed.begin_stage();
         if constexpr (l1 > l0) tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i], feed.template load<l0>(cbuf));
         else tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i]);
@@ -727,9 +733,11 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
   TileItem cur, next;
   if (!next_tile(cur)) return;
   typename Tk::Feed feed(a, (lptr)smem);
+  feed.look_ahead(cur);
   feed.init(cur);
   if constexpr (!STAGED) feed.prologue();
   bool more = next_tile(next);
+  if (more) feed.look_ahead(next);
   if constexpr (!STAGED) wait_loads<0>();
   for (;;) {
     TileItem after;
@@ -739,6 +747,7 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
       feed.init(next);
       if constexpr (!STAGED) feed.prologue();
       any_after = next_tile(after);  // while the loads are under way
+      if (any_after) feed.look_ahead(after);
     };
     const int n = (cur.ni + 31) / 32;
     static_for<WI>([&](auto ic) {

@@ -278,20 +278,30 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(const void* __restric
     dot[j] = 0.f;
   }
   const char* dr = (const char*)dout + (size_t)t * H * (OB ? 2 : 4);
+  // the loads of up to 8 of the rows are issued together: one after the other, a row's load behind the last row's
+  // products, the latencies of a small batch add up (16 tokens, top-8: 10 us)
+  constexpr int G = K < 8 ? K : 8;
   for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
     float d[8];
     load8<OB, V>(dr, c, H, d);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      if (rows[j] < 0) continue;
-      float v[8], o[8];
-      load8<false, V>(y + (size_t)rows[j] * H, c, H, v);
+    for (int j0 = 0; j0 < K; j0 += G) {
+      float v[G][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot[j] = fmaf(d[i], v[i], dot[j]);
-        o[i] = gate[j] * d[i];
+      for (int g = 0; g < G; ++g)
+        if (j0 + g < K) load8<false, V>(y + (size_t)max(rows[(j0 + g) % K], 0) * H, c, H, v[g]);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int j = (j0 + g) % K;
+        if (j0 + g >= K || rows[j] < 0) continue;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dot[j] = fmaf(d[i], v[g][i], dot[j]);
+          o[i] = gate[j] * d[i];
+        }
+        store8<YB, V>((char*)dy + (size_t)rows[j] * H * (YB ? 2 : 4), c, H, o);
       }
-      store8<YB, V>((char*)dy + (size_t)rows[j] * H * (YB ? 2 : 4), c, H, o);
     }
   }
 #pragma unroll
