@@ -44,11 +44,14 @@ struct Rows {
       row = base + off;
     }
   }
-  __device__ __forceinline__ u32x4 load(int c) const {
+  // whole: every lane's 16 bytes end inside the row, whose length is `total`
+  __device__ __forceinline__ u32x4 load(int c, bool whole, int total) const {
     if constexpr (DIRECT)
       return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(desc, c < len ? (int)(voff + c) : (int)kOutside, 0, 0));
-    else
-      return load_part<EB>(row + c, len - c);
+    if (total < 16) return load_part<EB>(row + c, len - c);
+    // (unconditional, as behind a condition the loads would wait for one another)
+    const u32x4 v = load_any(len ? row + min(c, len - 16) : (gptr)g_zero_page);
+    return whole ? v : shift_bytes(v, max(c - (len - 16), 0));
   }
 };
 
@@ -80,12 +83,13 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
   };
   const int c0 = (lane >> 4) * 16;
   auto load = [&](Group& G, int g) {
+    const bool whole = g * 128 + 128 <= len;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = g * 128 + h * 64 + c0;
-      G.w[h] = W.load(c);
+      G.w[h] = W.load(c, whole, len);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) G.x[h][m] = X[m].load(c);
+      for (int m = 0; m < MT; ++m) G.x[h][m] = X[m].load(c, whole, len);
     }
   };
   Acc acc[MT];

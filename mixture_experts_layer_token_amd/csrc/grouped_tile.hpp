@@ -149,7 +149,16 @@ struct Contig {
 #pragma unroll
     for (int q = 0; q < LQ; ++q) row[q] = rowp((q * kWaves + wave) * 8 + lane / 8);
   }
-  __device__ __forceinline__ u32x4 fetch(int q) const { return load_part<EB>(row[q] + c_byte, row[q] ? left - c_byte : 0); }
+  // Behind conditions the loads of a stage would wait for one another, so they are unconditional: a chunk that ends past
+  // the row reads the row's last 16 bytes, moved down afterwards (`adjust`), and a row of zeros reads a page of zeros.
+  // Rows of less than 16 bytes (TINY) are read element by element.
+  template <bool TINY>
+  __device__ __forceinline__ u32x4 fetch(int q) const {
+    if constexpr (TINY) return load_part<EB>(row[q] + c_byte, row[q] ? left - c_byte : 0);
+    return load_any(row[q] ? row[q] + min(c_byte, left - 16) : (gptr)g_zero_page);
+  }
+  __device__ __forceinline__ bool whole() const { return left >= kStageC; }
+  __device__ __forceinline__ u32x4 adjust(u32x4 v, int) const { return shift_bytes(v, max(c_byte - (left - 16), 0)); }
   __device__ __forceinline__ void end_fetch() {
 #pragma unroll
     for (int q = 0; q < LQ; ++q) row[q] += row[q] ? kStageC : 0;
@@ -230,9 +239,16 @@ struct Strided {
   __device__ __forceinline__ void init_fetch(gptr p, long long ld_bytes, int c_rows, int col_bytes) {
     base = p, ld64 = ld_bytes, left = c_rows, ncol = col_bytes;
   }
+  // (as in Contig: columns past the edge from the row's last 16 bytes, rows past the end from the last row)
+  template <bool TINY>
   __device__ __forceinline__ u32x4 fetch(int q, int wave, int lane) const {
     const int c = c_row(q, wave, lane), o = (int)col_of(q, wave, lane);
-    return load_part<EB>(base + c * ld64 + o, c < left ? ncol - o : 0);
+    if constexpr (TINY) return load_part<EB>(base + c * ld64 + o, c < left ? ncol - o : 0);
+    return load_any(base + min(c, left - 1) * ld64 + min(o, ncol - 16));
+  }
+  __device__ __forceinline__ bool whole() const { return left >= ROWS && ncol >= RB; }
+  __device__ __forceinline__ u32x4 adjust(u32x4 v, int q, int wave, int lane) const {
+    return shift_bytes(v, c_row(q, wave, lane) < left ? max((int)col_of(q, wave, lane) - (ncol - 16), 0) : 16);
   }
   __device__ __forceinline__ void end_fetch() {
     base += ld64 * ROWS;
@@ -440,28 +456,61 @@ struct TileKernel {
       idx_load(NB);
     }
 
+    // a stage into registers
     __device__ __forceinline__ void fetch() {
-#pragma unroll
-      for (int q = 0; q < OpA::LQ; ++q) {
-        if constexpr (SA) held[q] = A.fetch(q, wave, lane);
-        else held[q] = A.fetch(q);
-      }
-#pragma unroll
-      for (int q = 0; q < OpB::LQ; ++q) {
-        if constexpr (GATHER && OP == kOpDw) {
-          const int c = fetched * KE + OpB::c_row(q, wave, lane), o = (int)OpB::col_of(q, wave, lane);
-          const int xr = c < t.nc ? x_row(a, t.p0 + c) : -1;
-          held[OpA::LQ + q] =
-              load_part<EB>((gptr)a.x + ((size_t)max(xr, 0) * a.ldx + t.j0) * EB + o, xr >= 0 ? t.nj * EB - o : 0);
-        } else if constexpr (SB) {
-          held[OpA::LQ + q] = B.fetch(q, wave, lane);
-        } else {
-          held[OpA::LQ + q] = B.fetch(q);
-        }
-      }
+      const bool tiny_a = (OP == kOpY ? a.K : a.N) * EB < 16, tiny_b = a.K * EB < 16;  // bytes of the operands' rows
+      if (tiny_a || tiny_b) fetch_stage<true>();
+      else fetch_stage<false>();
       A.end_fetch();
       B.end_fetch();
       ++fetched;
+    }
+    template <bool TINY>
+    __device__ __forceinline__ void fetch_stage() {
+      constexpr bool GB = GATHER && OP == kOpDw;
+      int xr[GB ? OpB::LQ : 1];
+#pragma unroll
+      for (int q = 0; q < OpA::LQ; ++q) {
+        if constexpr (SA) held[q] = A.template fetch<TINY>(q, wave, lane);
+        else held[q] = A.template fetch<TINY>(q);
+      }
+#pragma unroll
+      for (int q = 0; q < OpB::LQ; ++q) {
+        if constexpr (GB) {
+          const int c = fetched * KE + OpB::c_row(q, wave, lane), p = a.perm_src[t.p0 + min(c, t.nc - 1)];
+          xr[q] = c < t.nc ? named_row(a, p) : -1;
+        } else if constexpr (SB) {
+          held[OpA::LQ + q] = B.template fetch<TINY>(q, wave, lane);
+        } else {
+          held[OpA::LQ + q] = B.template fetch<TINY>(q);
+        }
+      }
+      if constexpr (GB) {
+#pragma unroll
+        for (int q = 0; q < OpB::LQ; ++q) {
+          const int o = (int)OpB::col_of(q, wave, lane), ncol = t.nj * EB;
+          const gptr r = (gptr)a.x + ((size_t)max(xr[q], 0) * a.ldx + t.j0) * EB;
+          if constexpr (TINY) held[OpA::LQ + q] = load_part<EB>(r + o, xr[q] >= 0 ? ncol - o : 0);
+          else held[OpA::LQ + q] = load_any(xr[q] >= 0 ? r + min(o, ncol - 16) : (gptr)g_zero_page);
+        }
+      }
+      bool ok = A.whole() && B.whole();
+      if constexpr (GB) {
+        ok = ok && fetched * KE + KE <= t.nc;
+      }
+      if (TINY || ok) return;  // (uniform)
+#pragma unroll
+      for (int q = 0; q < OpA::LQ; ++q) {
+        if constexpr (SA) held[q] = A.adjust(held[q], q, wave, lane);
+        else held[q] = A.adjust(held[q], q);
+      }
+#pragma unroll
+      for (int q = 0; q < OpB::LQ; ++q) {
+        u32x4& h = held[OpA::LQ + q];
+        if constexpr (GB) h = shift_bytes(h, xr[q] >= 0 ? max((int)OpB::col_of(q, wave, lane) - (t.nj * EB - 16), 0) : 16);
+        else if constexpr (SB) h = B.adjust(h, q, wave, lane);
+        else h = B.adjust(h, q);
+      }
     }
     __device__ __forceinline__ void put(int buf) {
 #pragma unroll

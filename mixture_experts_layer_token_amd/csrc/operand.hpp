@@ -39,20 +39,35 @@ struct TileT<kF32> {
 // chunk added: a lane with this offset reads zeros.
 constexpr unsigned kOutside = 0xFFFFFC00u;
 
+// 16 bytes at any address
+__device__ __forceinline__ u32x4 load_any(gptr p) {
+  typedef u32x4 __attribute__((aligned(1))) any4;
+  return *(const __attribute__((address_space(1))) any4*)p;
+}
 // 16 bytes at any element-aligned address, of which the first n exist (the others are zeros)
 template <int EB>
 __device__ __forceinline__ u32x4 load_part(gptr p, int n) {
-  typedef u32x4 __attribute__((aligned(1))) any4;
   typedef typename std::conditional<EB == 1, unsigned char, typename std::conditional<EB == 2, unsigned short, unsigned>::type>::type El;
   u32x4 v = {0, 0, 0, 0};
   if (n >= 16) {
-    v = *(const __attribute__((address_space(1))) any4*)p;
+    v = load_any(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 16 / EB; ++i)
       if (i * EB < n) v[i * EB / 4] |= (unsigned)((const __attribute__((address_space(1))) El*)p)[i] << (i * EB % 4 * 8);
   }
   return v;
+}
+
+// v moved down by s bytes, zeros from above (s >= 16: zeros)
+__device__ __forceinline__ u32x4 shift_bytes(u32x4 v, int s) {
+  const unsigned long long lo = (unsigned long long)v[1] << 32 | v[0], hi = (unsigned long long)v[3] << 32 | v[2];
+  const int b = (s & 7) * 8;
+  const unsigned long long carry = b ? hi << (64 - b) : 0;
+  unsigned long long a = lo >> b | carry, c = hi >> b;
+  if (s >= 8) a = c, c = 0;
+  if (s >= 16) a = 0;
+  return u32x4{(unsigned)a, (unsigned)(a >> 32), (unsigned)c, (unsigned)(c >> 32)};
 }
 
 }  // namespace
