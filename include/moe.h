@@ -416,8 +416,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  *   x device, element type xdt; q device [rows][K] int8 (out); scale device [rows] fp32 (out)
  *   n_rows  device, one int32: only rows below it are read and written (offsets + E: the placed rows);
  *           NULL: all rows
- * Errors: MOE_ERR_INVALID (null pointers, bad type or act, rows < 0, K out of 1..1<<20, pointers that are
- * not element-aligned).
+ * q must not overlap x.  Errors: MOE_ERR_INVALID (null pointers, bad type or act, rows < 0, K out of
+ * 1..1<<20, pointers that are not element-aligned).
  */
 int moe_quant_rows(const void* x, int xdt, int rows, int K, int act, const int32_t* n_rows, int8_t* q, float* scale,
                    void* stream);
@@ -442,7 +442,8 @@ int moe_grouped_gemm_i8(const moe_grouped* g, const int8_t* q, const float* q_sc
  *   moe_swiglu_grad  dgu = [dh u s (1 + g (1 - s)) | dh g s],  s = 1 / (1 + e^-g);  and h again unless
  *                    h is NULL (so that a forward pass need not keep it)
  * fp32 arithmetic, one rounding to the type dt that all of them have.
- *   gu, dgu device [rows][2I]; h, dh device [rows][I]; n_rows as in moe_quant_rows
+ *   gu, dgu device [rows][2I]; h, dh device [rows][I]; n_rows as in moe_quant_rows; results must not
+ *   overlap operands
  * Errors: MOE_ERR_INVALID (null pointers, bad type, rows < 0, I out of 1..1<<20, pointers that are not
  * element-aligned).
  */
@@ -477,8 +478,10 @@ int moe_combine(const float* y_perm, const float* topk_w, const int32_t* inv_per
  *   dout device [T][H] of type odt; y_perm device [T*k][H] fp32; dy_perm device [T*k][H] of type ydt (out);
  *   dtopk_w device [T][k] fp32 (out); topk_ids device [T][k] int32 and dlogits device [T][E] fp32 (out),
  *   or both NULL
- * fp32 sums in a fixed order.  Errors: MOE_ERR_INVALID (null pointers, bad types, sizes out of range
- * (E out of 1..1024 with dlogits), dlogits without topk_ids, pointers that are not element-aligned).
+ * fp32 sums in a fixed order; dy_perm must not overlap dout or y_perm, and no two pairs may have one position.
+ * Errors: MOE_ERR_INVALID (null pointers, bad types, sizes out of range (E out of 1..1024 with dlogits),
+ * dlogits without topk_ids, pointers that are not element-aligned), MOE_ERR_UNSUPPORTED (more than 2^32
+ * threads in one launch: T >= 2^23 or more).
  */
 int moe_combine_grad(const void* dout, int odt, const float* y_perm, const float* topk_w, const int32_t* inv_perm,
                      int T, int k, int H, void* dy_perm, int ydt, float* dtopk_w, const int32_t* topk_ids, int E,

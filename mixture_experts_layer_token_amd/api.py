@@ -267,10 +267,14 @@ def _same_dt(a, b):
     return _dt(a)
 
 
-def _grouped_ws(ws, dt, g, device):
+def _grouped_ws(ws, dt, g, device, stream):
     if ws is None:
         need = int(lib().moe_grouped_workspace(dt, g.rows, g.N, g.K, g.E))
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            if stream is not None:  # used there, allocated (and freed on return) on the current stream
+                stream.wait_stream(torch.cuda.current_stream(device))
+                ws.record_stream(stream)
     return ws, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
 
 
@@ -278,7 +282,7 @@ def moe_grouped_gemm(x, w, offsets, y, perm_src=None, k=1, ws=None, stream=None)
     """y[p] = w[e] x[r(p)] for the rows p of every expert e.  `ws`: device workspace of at least
     moe_grouped_workspace bytes (allocated here if None)."""
     g, dt = _grouped(x, w, y, offsets, perm_src, k), _same_dt(x, w)
-    ws, wp, wn = _grouped_ws(ws, dt, g, x.device)
+    ws, wp, wn = _grouped_ws(ws, dt, g, x.device, stream)
     _launch(lib().moe_grouped_gemm, (ctypes.byref(g), dt, _rowp(x), _rowp(w), _rowp(y), _dt(y), wp, wn),
             (x, w, y, offsets, perm_src, ws), stream)
 
@@ -286,7 +290,7 @@ def moe_grouped_gemm(x, w, offsets, y, perm_src=None, k=1, ws=None, stream=None)
 def moe_grouped_gemm_dx(dy, w, offsets, dx, ws=None, stream=None):
     """dx[p] = w[e]^T dy[p]: the gradient of the grouped rows."""
     g, dt = _grouped(dx, w, dy, offsets, None, 1), _same_dt(dy, w)
-    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device)
+    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device, stream)
     _launch(lib().moe_grouped_gemm_dx, (ctypes.byref(g), dt, _rowp(dy), _rowp(w), _rowp(dx), _dt(dx), wp, wn),
             (dy, w, dx, offsets, ws), stream)
 
@@ -294,7 +298,7 @@ def moe_grouped_gemm_dx(dy, w, offsets, dx, ws=None, stream=None):
 def moe_grouped_gemm_dw(dy, x, offsets, dw, perm_src=None, k=1, ws=None, stream=None):
     """dw[e] = sum over the rows p of expert e of dy[p] x[r(p)]^T: the gradient of the weights."""
     g, dt = _grouped(x, dw, dy, offsets, perm_src, k), _same_dt(dy, x)
-    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device)
+    ws, wp, wn = _grouped_ws(ws, dt, g, dy.device, stream)
     _launch(lib().moe_grouped_gemm_dw, (ctypes.byref(g), dt, _rowp(dy), _rowp(x), _rowp(dw), _dt(dw), wp, wn),
             (dy, x, dw, offsets, perm_src, ws), stream)
 

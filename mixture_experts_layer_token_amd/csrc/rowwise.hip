@@ -97,14 +97,14 @@ __device__ __forceinline__ int quantize(float v, int e, float top, float inv) {
 // between the maximum and the rounding when it fits CH chunks of 8 per lane; else (CH = 0) they are read
 // (and gated) a second time.
 template <bool BF16, bool GATE, bool V, int WPR, int CH>
-__global__ __launch_bounds__(256) void quant_kernel(const void* __restrict__ x, int rows, int K,
+__global__ __launch_bounds__(256) void quant_kernel(const void* __restrict__ x, int row0, int rows, int K,
                                                     const int32_t* __restrict__ n_rows, int8_t* __restrict__ q,
                                                     float* __restrict__ scale) {
   constexpr int LPR = 64 * WPR, C = CH > 0 ? CH : 1;
   __shared__ float s_max[4];
   __shared__ int s_bad[4];
   const int lane = threadIdx.x % LPR;
-  const int r = blockIdx.x * (4 / WPR) + threadIdx.x / LPR;
+  const int r = row0 + blockIdx.x * (4 / WPR) + threadIdx.x / LPR;
   if (r >= row_limit(rows, n_rows)) return;  // uniform over the lanes of a row (WPR = 4: over the workgroup)
   const char* xr = (const char*)x + (size_t)r * K * (GATE ? 2 : 1) * (BF16 ? 2 : 4);
   const char* xu = xr + (size_t)K * (BF16 ? 2 : 4);
@@ -183,18 +183,27 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* __restrict__ x, 
 }
 
 template <bool BF16, bool GATE, bool V>
-void quant_any(const void* x, int rows, int K, const int32_t* n_rows, int8_t* q, float* scale, hipStream_t s) {
-  const dim3 one((rows + 3) / 4), all(rows), b(256);
+void quant_some(const void* x, int row0, int count, int rows, int K, const int32_t* n_rows, int8_t* q, float* scale,
+                hipStream_t s) {
+  const dim3 one((count + 3) / 4), all(count), b(256);
   if (K <= 512)
-    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 1, 1>), one, b, 0, s, x, rows, K, n_rows, q, scale);
+    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 1, 1>), one, b, 0, s, x, row0, rows, K, n_rows, q, scale);
   else if (K <= 2048)
-    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 1>), all, b, 0, s, x, rows, K, n_rows, q, scale);
+    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 1>), all, b, 0, s, x, row0, rows, K, n_rows, q, scale);
   else if (K <= 4096)
-    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 2>), all, b, 0, s, x, rows, K, n_rows, q, scale);
+    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 2>), all, b, 0, s, x, row0, rows, K, n_rows, q, scale);
   else if (K <= 16384)
-    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 8>), all, b, 0, s, x, rows, K, n_rows, q, scale);
+    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 8>), all, b, 0, s, x, row0, rows, K, n_rows, q, scale);
   else
-    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 0>), all, b, 0, s, x, rows, K, n_rows, q, scale);
+    hipLaunchKernelGGL((quant_kernel<BF16, GATE, V, 4, 0>), all, b, 0, s, x, row0, rows, K, n_rows, q, scale);
+}
+
+// (a launch holds 2^32 threads, the rows of all experts' weights may be more than 2^24)
+template <bool BF16, bool GATE, bool V>
+void quant_any(const void* x, int rows, int K, const int32_t* n_rows, int8_t* q, float* scale, hipStream_t s) {
+  constexpr int kRows = 1 << 23;
+  for (int r = 0; r < rows; r += std::min(kRows, rows - r))
+    quant_some<BF16, GATE, V>(x, r, std::min(kRows, rows - r), rows, K, n_rows, q, scale, s);
 }
 
 // ------------------------------------------------------------------ SwiGLU gate
@@ -260,13 +269,13 @@ void swiglu_any(const void* gu, const void* dh, int rows, int I, const int32_t* 
 // products of its columns and keeps k partial dot products, which are summed over the workgroup in a fixed
 // order.  The gates' softmax gradient needs all k of them and follows in the same workgroup.
 template <bool OB, bool YB, bool V, int K>
-__global__ __launch_bounds__(512) void combine_grad_kernel(const void* __restrict__ dout, const float* __restrict__ y,
+__global__ __launch_bounds__(1024) void combine_grad_kernel(const void* __restrict__ dout, const float* __restrict__ y,
                                                            const float* __restrict__ w,
                                                            const int32_t* __restrict__ inv, int T, int H,
                                                            void* __restrict__ dy, float* __restrict__ dw,
                                                            const int32_t* __restrict__ ids, int E,
                                                            float* __restrict__ dlogits) {
-  __shared__ float part[8][K], total[K];
+  __shared__ float part[16][K], total[K];
   const int t = blockIdx.x;
   int rows[K];
   float gate[K], dot[K];
@@ -332,59 +341,6 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(const void* __restric
   }
 }
 
-// The same for a batch of few tokens: one workgroup per pair, so that more than T compute units work; the gates'
-// gradient follows in a launch of its own.
-template <bool OB, bool YB, bool V>
-__global__ __launch_bounds__(256) void combine_grad_pair_kernel(const void* __restrict__ dout,
-                                                                const float* __restrict__ y,
-                                                                const float* __restrict__ w,
-                                                                const int32_t* __restrict__ inv, int k, int n, int H,
-                                                                void* __restrict__ dy, float* __restrict__ dw) {
-  __shared__ float part[4];
-  const int i = blockIdx.x, p = inv[i];
-  if ((unsigned)p >= (unsigned)n) {
-    if (threadIdx.x == 0) dw[i] = 0.f;
-    return;
-  }
-  const float gate = w[i];
-  const char* dr = (const char*)dout + (size_t)(i / k) * H * (OB ? 2 : 4);
-  float dot = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
-    float d[8], v[8], o[8];
-    load8<OB, V>(dr, c, H, d);
-    load8<false, V>(y + (size_t)p * H, c, H, v);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      dot = fmaf(d[q], v[q], dot);
-      o[q] = gate * d[q];
-    }
-    store8<YB, V>((char*)dy + (size_t)p * H * (YB ? 2 : 4), c, H, o);
-  }
-#pragma unroll
-  for (int off = 32; off; off >>= 1) dot += __shfl_xor(dot, off, 64);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float v = 0.f;
-    for (int q = 0; q < (int)blockDim.x / 64; ++q) v += part[q];
-    dw[i] = v;
-  }
-}
-__global__ __launch_bounds__(256) void gate_grad_kernel(const float* __restrict__ w, const float* __restrict__ dw,
-                                                        const int32_t* __restrict__ inv, const int32_t* __restrict__ ids,
-                                                        int k, int n, int E, float* __restrict__ dlogits) {
-  const size_t t = blockIdx.x;
-  float mean = 0.f;
-  for (int j = 0; j < k; ++j)
-    if ((unsigned)inv[t * k + j] < (unsigned)n) mean = fmaf(w[t * k + j], dw[t * k + j], mean);
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    float v = 0.f;
-    for (int j = 0; j < k; ++j)
-      if ((unsigned)inv[t * k + j] < (unsigned)n && ids[t * k + j] == e) v += w[t * k + j] * (dw[t * k + j] - mean);
-    dlogits[t * E + e] = v;
-  }
-}
-
 template <bool OB, bool YB, bool V, int... Ks>
 void combine_grad_any(int k, unsigned T, int threads, const void* dout, const float* y, const float* w,
                       const int32_t* inv, int H, void* dy, float* dw, const int32_t* ids, int E, float* dlogits,
@@ -435,19 +391,15 @@ int launch_combine_grad(const void* dout, int odt, const float* y, const float* 
                         int H, void* dy, int ydt, float* dw, const int32_t* ids, int E, float* dlogits,
                         hipStream_t s) {
   const bool v = H % 8 == 0 && al16(dout) && al16(y) && al16(dy);
-  // fewer tokens than compute units: by pairs (16 tokens, top-8, H = 7168: 10.7 -> 8.5 us)
-  const bool by_pair = T < 128 && k > 1;
-  int threads = by_pair ? 256 : 512;
+  // fewer tokens than compute units: more lanes for each, so that a row takes one pass (16 tokens, top-8, H = 7168:
+  // 10.7 -> 9.9 us)
+  int threads = T < 256 ? 1024 : 512;
   while (threads > 64 && threads * 8 > H) threads >>= 1;
+  while (threads < 1024 && threads * 8 < H && T < 256) threads <<= 1;
+  if ((long long)T * threads > 0xFFFFFFFFLL) return fail(MOE_ERR_UNSUPPORTED, "moe_combine_grad: T=%d in one launch", T);
   auto go = [&](auto ob, auto yb) {
     constexpr bool OB = decltype(ob)::value, YB = decltype(yb)::value;
-    if (by_pair && v)
-      hipLaunchKernelGGL((combine_grad_pair_kernel<OB, YB, true>), dim3(T * k), dim3(threads), 0, s, dout, y, w, inv, k,
-                         T * k, H, dy, dw);
-    else if (by_pair)
-      hipLaunchKernelGGL((combine_grad_pair_kernel<OB, YB, false>), dim3(T * k), dim3(threads), 0, s, dout, y, w, inv, k,
-                         T * k, H, dy, dw);
-    else if (v)
+    if (v)
       combine_grad_any<OB, YB, true>(k, (unsigned)T, threads, dout, y, w, inv, H, dy, dw, ids, E, dlogits, s,
                                      std::make_integer_sequence<int, 16>{});
     else
@@ -459,10 +411,6 @@ int launch_combine_grad(const void* dout, int odt, const float* y, const float* 
   else
     ydt == MOE_BF16 ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
   MOE_CHECK_LAUNCH("moe_combine_grad launch");
-  if (by_pair && dlogits) {
-    hipLaunchKernelGGL(gate_grad_kernel, dim3(T), dim3(256), 0, s, w, dw, inv, ids, k, T * k, E, dlogits);
-    MOE_CHECK_LAUNCH("moe_combine_grad launch");
-  }
   return MOE_OK;
 }
 

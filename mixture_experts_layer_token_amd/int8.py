@@ -51,6 +51,8 @@ class MoeInt8Layer:
 
     def forward(self, x, out=None):
         """One layer forward on the current stream (x [T, H] in the router's type)."""
+        if x.dim() != 2 or x.shape[1] != self.H or x.dtype != self.w_router.dtype:
+            raise ValueError("x %s %s: %s [T, %d] expected" % (x.dtype, tuple(x.shape), self.w_router.dtype, self.H))
         T, k = x.shape[0], self.k
         if T > self.max_T:
             self._alloc(T)

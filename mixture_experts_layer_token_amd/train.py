@@ -114,4 +114,8 @@ class MoeTrainLayer(torch.nn.Module):
         self.w_down = par(E, H, I)
 
     def forward(self, x):
+        if x.dim() != 2 or x.shape[1] != self.w_router.shape[1]:
+            raise ValueError("x %s: [T, %d] expected" % (tuple(x.shape), self.w_router.shape[1]))
+        if any(p.dtype != x.dtype for p in (self.w_router, self.w_gate_up, self.w_down)):
+            raise TypeError("x and the weights must have one type (x: %s)" % x.dtype)
         return _MoeLayerFunction.apply(x, self.w_router, self.bias, self.w_gate_up, self.w_down, self.k)

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 import mixture_experts_layer_token_amd as moe  # noqa: E402
 
 import grouped_ref as R  # noqa: E402
+from grouped_ref import f64  # noqa: E402
 from helpers import say  # noqa: E402
 
 
@@ -366,3 +367,117 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for o, r in zip(outs, refs):
         assert torch.equal(o, r)
+
+
+def test_rows_past_four_gigabytes():
+    """x rows, results and weights whose byte offsets do not fit 32 bits."""
+    K, N, rows = 4096, 64, 40
+    T = (1 << 32) // (K * 2) + 1000
+    x = torch.empty((T, K), device="cuda", dtype=torch.bfloat16)
+    picks = torch.tensor([0, 1, T - 1, T - 2, T // 2, T - 999] * 7, dtype=torch.int32, device="cuda")[:rows]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    vals = torch.randn((rows, K), generator=gen, device="cuda").bfloat16()
+    x[picks.long()] = vals
+    named = x[picks.long()]  # (a row picked twice holds one of its values)
+    w = torch.randn((2, N, K), generator=gen, device="cuda").bfloat16()
+    dy = torch.randn((rows, N), generator=gen, device="cuda").bfloat16()
+    off = np.array([0, 25, rows], np.int32)
+    offsets = torch.from_numpy(off).cuda()
+    y, dw = torch.empty((rows, N), device="cuda"), torch.empty((2, N, K), device="cuda")
+    moe.moe_grouped_gemm(x, w, offsets, y, perm_src=picks * 2, k=2)
+    moe.moe_grouped_gemm_dw(dy, x, offsets, dw, perm_src=picks * 2, k=2)
+    torch.cuda.synchronize()
+    R.assert_product(y, *R.product("y", f64(named), f64(w), None, off), what="y")
+    R.assert_product(dw, *R.product("dw", f64(named), None, f64(dy), off), what="dw")
+    # grouped rows in place: the last group lies past 4 GiB
+    g2 = torch.tensor([0, 3, T - 30], dtype=torch.int32)
+    offs = torch.cat([g2, torch.tensor([T], dtype=torch.int32)])
+    w3 = torch.randn((3, N, K), generator=gen, device="cuda").bfloat16()
+    x[:3], x[T - 30:] = vals[:3], vals[3:33]
+    x[3:T - 30] = 0
+    y2 = torch.full((T, N), SENTINEL, device="cuda", dtype=torch.bfloat16)
+    moe.moe_grouped_gemm(x, w3, offs.cuda(), y2)
+    torch.cuda.synchronize()
+    assert (y2[3:T - 30] == 0).all()
+    tail = f64(vals[3:33]) @ f64(w3[2]).T
+    R.assert_product(y2[T - 30:], tail, f64(vals[3:33]).abs() @ f64(w3[2]).abs().T, K, "tail")
+
+
+def test_explicit_stream_allocates_its_workspace_safely():
+    counts, N, K = GROUPS["skinny"]
+    c = make("skinny", torch.bfloat16)
+    assert moe.moe_grouped_workspace("bf16", c["rows"], N, K, c["E"]) > 0  # few tiles, many rows: split sums
+    dw, ref = (torch.empty((c["E"], N, K), device="cuda") for _ in range(2))
+    moe.moe_grouped_gemm_dw(c["dy"], c["x"], c["offsets"], ref)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    moe.moe_grouped_gemm_dw(c["dy"], c["x"], c["offsets"], dw, stream=s)
+    junk = torch.full((1 << 22,), 3.0, device="cuda")  # would take the freed workspace's place
+    torch.cuda.synchronize()
+    assert torch.equal(dw, ref) and float(junk[0]) == 3.0
+
+
+def reference_on_gpu(op, x, w, y, off):
+    """R.product with 64-bit products on the device (sizes for which the CPU would take minutes)."""
+    E = len(off) - 1
+    N, K = y.shape[1], x.shape[1]
+    shape = {"y": y.shape, "dx": x.shape, "dw": (E, N, K)}[op]
+    out, mag = (torch.zeros(shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        a, b = {"y": lambda: (x[r].double(), w[e].double().T), "dx": lambda: (y[r].double(), w[e].double()),
+                "dw": lambda: (y[r].double().T, x[r].double())}[op]()
+        d = e if op == "dw" else r
+        out[d], mag[d] = a @ b, a.abs() @ b.abs()
+    return out.cpu(), mag.cpu(), {"y": K, "dx": N, "dw": max(1, int(np.diff(off).max()))}[op]
+
+
+# several rounds of 256 x 256 tiles, odd ends everywhere: the shape of long calls
+@pytest.mark.parametrize("op,N,K", [("y", 8200, 584), ("dx", 584, 8200), ("dw", 4104, 4136)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_large_tiles(op, N, K, gather):
+    say("grouped large", op, N, K, gather)
+    counts = [3000, 0, 5101, 92]
+    off = R.offsets_of(counts)
+    rows, E, k = sum(counts), len(counts), 2 if gather else 1
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(21)
+    x = torch.randn((rows, K), generator=gen, device="cuda").bfloat16()
+    w = torch.randn((E, N, K), generator=gen, device="cuda").bfloat16()
+    dy = torch.randn((rows, N), generator=gen, device="cuda").bfloat16()
+    perm = torch.randint(0, rows * k, (rows,), generator=gen, device="cuda", dtype=torch.int32) if gather else None
+    kw = dict(perm_src=perm, k=k) if gather else {}
+    xg = x[(perm // k).long()] if gather else x
+    offsets = torch.from_numpy(off).cuda()
+    for dt in (torch.float32, torch.bfloat16):
+        if op == "y":
+            out = torch.empty((rows, N), device="cuda", dtype=dt)
+            moe.moe_grouped_gemm(x, w, offsets, out, **kw)
+        elif op == "dx":
+            out = torch.empty((rows, K), device="cuda", dtype=dt)
+            moe.moe_grouped_gemm_dx(dy, w, offsets, out)
+        else:
+            out = torch.empty((E, N, K), device="cuda", dtype=dt)
+            moe.moe_grouped_gemm_dw(dy, x, offsets, out, **kw)
+        torch.cuda.synchronize()
+        R.assert_product(out, *reference_on_gpu(op, xg, w, dy, off), what=op)
+
+
+def test_large_int8_tiles():
+    counts, N, K = [3000, 0, 5101, 92], 8200, 592
+    off = R.offsets_of(counts)
+    rows, E = sum(counts), len(counts)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(22)
+    q = torch.randint(-128, 128, (rows, K), generator=gen, device="cuda").to(torch.int8)
+    w = torch.randint(-128, 128, (E, N, K), generator=gen, device="cuda").to(torch.int8)
+    qs, ws = torch.rand(rows, generator=gen, device="cuda") + 0.1, torch.rand((E, N), generator=gen, device="cuda") + 0.1
+    y = torch.empty((rows, N), device="cuda")
+    moe.moe_grouped_gemm_i8(q, qs, w, ws, torch.from_numpy(off).cuda(), y)
+    torch.cuda.synchronize()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        v = (q[r].double() @ w[e].double().T) * qs[r, None].double() * ws[e].double()
+        # the conversion of the exact sum and two products in fp32: 2^-24 each
+        assert bool(((y[r].double() - v).abs() <= v.abs() * 3.0001 * 2.0 ** -24).all())
