@@ -8,14 +8,22 @@ namespace moe {
 namespace {
 
 // How many parts the rows of each group are cut into for a weight gradient: its tiles of 128 x 128 alone would leave
-// compute units idle, and a part keeps at least 256 rows.  (The router's gradient, 128 x 2880 over 4096 rows in fp32: 23
-// tiles.)
-int dw_split(int rows, int N, int K, int E) {
+// compute units idle.  A part keeps at least 256 rows, and two parts share a compute unit at most.  fp32 parts are bound by
+// the matrix cores, so two on one unit take twice as long as one and the units with one wait: of the counts that keep the
+// busiest unit's share of the rows smallest, the least.  (128 x 2880 over 4096 rows, 23 tiles: in 16 parts each 48 us, in
+// 11 41; 384 x 7168, 168 tiles: whole 248 us, in 3 parts 187.)  bf16 parts wait on memory and take all that fit.
+int dw_split(int type, int rows, int N, int K, int E) {
   const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
   if (tiles >= 256) return 1;
   const long long by_rows = (long long)rows / E / 256, by_tiles = 512 / tiles;
-  const long long s = by_rows < by_tiles ? by_rows : by_tiles;
-  return s < 2 ? 1 : s > 16 ? 16 : (int)s;
+  const int most = (int)(by_rows < by_tiles ? by_rows : by_tiles);
+  if (type != kF32) return most < 2 ? 1 : most > 32 ? 32 : most;
+  int best = 1, share = 1;  // the busiest unit holds share parts of best
+  for (int s = 2; s <= most && s <= 32; s++) {
+    const int n = (int)((tiles * s + 255) / 256);
+    if (n * best < share * s) best = s, share = n;
+  }
+  return best;
 }
 
 // dw = sum over the parts, in order: one thread per element (the partial sums are at most 32 MiB: 512 tiles)
@@ -50,8 +58,8 @@ TileShape cheapest_shape(const GroupArgs& a, int op, int eb, double large, doubl
 
 }  // namespace
 
-size_t grouped_workspace(int, int rows, int N, int K, int E) {
-  const int s = dw_split(rows, N, K, E);
+size_t grouped_workspace(int type, int rows, int N, int K, int E) {
+  const int s = dw_split(type, rows, N, K, E);
   return s > 1 ? ((size_t)s * E * N * K * 4 + 255) / 256 * 256 : 0;
 }
 
@@ -74,7 +82,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
       return launch_grouped_decode(a, type, t == kLarge, s);
   }
   if (op == kOpDw) {
-    const int split = dw_split(a.rows, a.N, a.K, a.E);
+    const int split = dw_split(type, a.rows, a.N, a.K, a.E);
     if (split > 1) {
       if (t == kLarge) t = kDeep;
       GroupArgs p = a;

@@ -47,8 +47,7 @@ __device__ __forceinline__ int named_row(const GroupArgs& a, int s) {
 // x row of grouped row p (p < rows), or -1
 __device__ __forceinline__ int x_row(const GroupArgs& a, int p) { return a.perm_src ? named_row(a, a.perm_src[p]) : p; }
 
-// Row tiles of mr rows over the groups in expert order; at most this many exist for any offsets whose
-// groups do not overlap (launch bound: overlapping groups are cut off there).
+// Most row tiles of mr rows that groups which do not overlap can have (the bound of the launch).
 inline long long group_tiles_max(int rows, int E, int mr) {
   return (long long)rows / mr + (rows < E ? rows : E);
 }
