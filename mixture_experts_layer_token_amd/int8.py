@@ -23,13 +23,19 @@ def quantize_weights(w: torch.Tensor):
 
 class MoeInt8Layer:
     """`w_gate_up` [E, 2I, H] (gate rows, then up rows) and `w_down` [E, H, I] are quantized here; the router stays in
-    its own type.  All buffers are allocated once for batches of up to max_T tokens."""
+    its own type.  All buffers are allocated once for batches of up to max_T tokens (a larger batch allocates more; graphs
+    captured before keep theirs), so one forward runs at a time."""
 
     def __init__(self, w_router, bias, w_gate_up, w_down, k, max_T=1):
         self.w_router, self.bias, self.k = w_router, bias, k
         self.E, self.H, self.I = w_gate_up.shape[0], w_gate_up.shape[2], w_down.shape[2]
         if tuple(w_gate_up.shape) != (self.E, 2 * self.I, self.H) or tuple(w_down.shape) != (self.E, self.H, self.I):
             raise ValueError("w_gate_up %s and w_down %s do not fit" % (tuple(w_gate_up.shape), tuple(w_down.shape)))
+        if tuple(w_router.shape) != (self.E, self.H):
+            raise ValueError("w_router %s: [%d, %d] expected" % (tuple(w_router.shape), self.E, self.H))
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (self.E,)):
+            raise ValueError("bias %s %s: float32 [%d] expected" % (bias.dtype, tuple(bias.shape), self.E))
+        self._outgrown = []
         self.gate_up = quantize_weights(w_gate_up)
         self.down = quantize_weights(w_down)
         self._alloc(max_T)
@@ -53,14 +59,25 @@ class MoeInt8Layer:
         """One layer forward on the current stream (x [T, H] in the router's type)."""
         if x.dim() != 2 or x.shape[1] != self.H or x.dtype != self.w_router.dtype:
             raise ValueError("x %s %s: %s [T, %d] expected" % (x.dtype, tuple(x.shape), self.w_router.dtype, self.H))
-        T, k = x.shape[0], self.k
-        if T > self.max_T:
-            self._alloc(T)
+        T = x.shape[0]
+        if x.device != self.w_router.device:
+            raise ValueError("x is on %s, the layer on %s" % (x.device, self.w_router.device))
         if out is None:
             out = torch.empty_like(x)
+        elif out.shape != x.shape or out.device != x.device:
+            raise ValueError("out %s on %s: that of x expected" % (tuple(out.shape), out.device))
+        if T > self.max_T:
+            self._outgrown.append((self.ids, self.gates, self.counts, self.offsets, self.perm, self.inv, self.q,
+                                   self.q_scale, self.gu, self.h, self.h_scale, self.y, self.rws))
+            self._alloc(T)
         if T == 0:
             return out
-        n = T * k
+        with torch.cuda.device(x.device):
+            self._run(x, out, T)
+        return out
+
+    def _run(self, x, out, T):
+        k, n = self.k, T * self.k
         ids, gates, perm, inv = self.ids[:T], self.gates[:T], self.perm[:n], self.inv[:n]
         api.moe_route_permute(x, self.w_router, self.bias, k, ids, gates, self.counts, self.offsets, perm, inv,
                               ws=self.rws)
@@ -69,4 +86,3 @@ class MoeInt8Layer:
         api.moe_quant_rows(self.gu[:n], self.h[:n], self.h_scale[:n], act="swiglu", n_rows=self.offsets[-1:])
         api.moe_grouped_gemm_i8(self.h[:n], self.h_scale[:n], *self.down, self.offsets, self.y[:n])
         api.moe_combine(self.y[:n], gates, inv, k, None, out)
-        return out

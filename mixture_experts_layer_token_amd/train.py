@@ -71,14 +71,17 @@ class _MoeLayerFunction(torch.autograd.Function):
                 dw_gate_up = torch.empty_like(w_gate_up, memory_format=torch.contiguous_format)
                 api.moe_grouped_gemm_dw(dgu, x, offsets, dw_gate_up, perm_src=perm, k=k)
         # the router: one group of all tokens, in fp32
-        if need_x or need_r:
+        if need_x or need_r or need_b:
             all_rows = _one_group(T, dev)
         if need_r:
             dwr = torch.empty((1, E, H), dtype=f32, device=dev)
             api.moe_grouped_gemm_dw(dlogits, x.to(f32), all_rows, dwr)
             dw_router = dwr[0].to(w_router.dtype)
         if need_b and ctx.has_bias:
-            dbias = dlogits.sum(dim=0)
+            # the sum over the tokens as a product with ones: fixed order, and no memset node when captured
+            column = torch.empty((1, E, 1), dtype=f32, device=dev)
+            api.moe_grouped_gemm_dw(dlogits, torch.ones((T, 1), dtype=f32, device=dev), all_rows, column)
+            dbias = column.view(E)
         if need_x:
             rows = torch.empty((n, H), dtype=f32, device=dev)
             api.moe_grouped_gemm_dx(dgu, w_gate_up, offsets, rows)
@@ -95,7 +98,8 @@ def _one_group(rows, device):
 
 
 class MoeTrainLayer(torch.nn.Module):
-    """Routed-expert SwiGLU layer with plain parameters; x and all weights in one type, bfloat16 or float32."""
+    """Routed-expert SwiGLU layer with plain parameters; x and all weights in one type, bfloat16 or float32 (the
+    router's bias is float32 with either)."""
 
     def __init__(self, H, I, E, k, dtype=torch.bfloat16, bias=False, device="cuda", sigma=0.02):
         super().__init__()
@@ -116,6 +120,11 @@ class MoeTrainLayer(torch.nn.Module):
     def forward(self, x):
         if x.dim() != 2 or x.shape[1] != self.w_router.shape[1]:
             raise ValueError("x %s: [T, %d] expected" % (tuple(x.shape), self.w_router.shape[1]))
+        if any(p.device != x.device for p in self.parameters()):
+            raise ValueError("x is on %s, a parameter is not" % x.device)
         if any(p.dtype != x.dtype for p in (self.w_router, self.w_gate_up, self.w_down)):
             raise TypeError("x and the weights must have one type (x: %s)" % x.dtype)
-        return _MoeLayerFunction.apply(x, self.w_router, self.bias, self.w_gate_up, self.w_down, self.k)
+        if self.bias is not None and self.bias.dtype != torch.float32:
+            raise TypeError("the router's bias stays float32, got %s" % self.bias.dtype)
+        with torch.cuda.device(x.device):
+            return _MoeLayerFunction.apply(x, self.w_router, self.bias, self.w_gate_up, self.w_down, self.k)
