@@ -481,3 +481,25 @@ def test_large_int8_tiles():
         v = (q[r].double() @ w[e].double().T) * qs[r, None].double() * ws[e].double()
         # the conversion of the exact sum and two products in fp32: 2^-24 each
         assert bool(((y[r].double() - v).abs() <= v.abs() * 3.0001 * 2.0 ** -24).all())
+
+
+# weight gradients with few tiles: the rows in up to 32 parts, some parts without rows, a column of ones (a plain sum)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K", [([9001], 16, 1), ([9001], 24, 40), ([4099, 2], 136, 200), ([1, 0, 6000], 8, 520),
+                                        ([1025], 390, 1030)])
+def test_weight_gradients_in_parts(counts, N, K, dt):
+    say("grouped parts", counts, N, K, dt)
+    off = R.offsets_of(counts)
+    rows, E = sum(counts) + 5, len(counts)  # 5 rows behind the last group
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(31)
+    x = torch.randn((rows, K), generator=gen, device="cuda").to(dt)
+    dy = torch.randn((rows, N), generator=gen, device="cuda").to(dt)
+    need = moe.moe_grouped_workspace("f32" if dt == torch.float32 else "bf16", rows, N, K, E)
+    assert need >= 2 * E * N * K * 4
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever a part is not written
+    for out in (torch.float32, torch.bfloat16):
+        dw = torch.empty((E, N, K), device="cuda", dtype=out)
+        moe.moe_grouped_gemm_dw(dy, x, torch.from_numpy(off).cuda(), dw, ws=ws)
+        torch.cuda.synchronize()
+        R.assert_product(dw, *reference_on_gpu("dw", x, None, dy, off), what="dw")
