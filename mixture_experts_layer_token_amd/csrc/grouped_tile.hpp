@@ -84,35 +84,52 @@ constexpr int kWaves = 4;
 // The loads are inline assembly (they have no result register: the data goes to LDS): after the compiler's own
 // LDS-direct loads, every transposing LDS read would wait for all loads in flight.  `Load` is one of them, kept
 // until it is written out, on its own or around an MFMA, which then separates the write of m0 from its use.
+// Where scalar registers are short a descriptor word waits in a vector register, and the v_readfirstlane that brings it
+// back may stand right before the assembly, in which the compiler inserts nothing; a buffer instruction may read a scalar
+// register 5 wait states after a vector instruction wrote it.  So the assembly of the first load of an operand and stage (a
+// descriptor is made once for all of them) and of every load on its own waits by itself.  (On every load around an
+// MFMA: forward product of 8192 rows over 8 experts of 28672 x 4096 1.62 -> 1.65 ms, in turn on one card.)  The generated code is checked.
 struct Load {
   u32x4 desc;
   unsigned voff, lds;
 };
 __device__ __forceinline__ Load make_load(gptr base, unsigned bytes, unsigned voff, lptr l) {
   const unsigned long long p = (unsigned long long)base;
-  // (uniform already: this only keeps the compiler from holding them in vector registers)
+  // (uniform: assembly operands have to be scalar registers, wherever the compiler has kept the values)
   auto u = [](unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); };
   return Load{u32x4{u((unsigned)p), u((unsigned)(p >> 32)) & 0xFFFFu, u(bytes), 0x00027000u}, voff,
               u((unsigned)(size_t)l)};
 }
 __device__ __forceinline__ void load_now(const Load& d) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                : : "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
-template <int E>
+template <int E, bool FIRST>
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const bf16x8& b, const bf16x8& a, const Load& d) {
-  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
-               : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\ts_nop 2\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
-template <int E>
+template <int E, bool FIRST>
 __device__ __forceinline__ void tile_mfma(i32x4& acc, const i32x4& b, const i32x4& a, const Load& d) {
-  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
-               : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\ts_nop 2\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b), "v"(a), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
-template <int E>
+template <int E, bool FIRST>
 __device__ __forceinline__ void tile_mfma(f32x4& acc, const f32x4& b, const f32x4& a, const Load& d) {
-  asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x4_f32 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
-               : "+a"(acc) : "v"(b[E]), "v"(a[E]), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x4_f32 %0, %1, %2, %0\n\ts_nop 2\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b[E]), "v"(a[E]), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\tv_mfma_f32_16x16x4_f32 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                 : "+a"(acc) : "v"(b[E]), "v"(a[E]), "s"(d.lds), "v"(d.voff), "s"(d.desc) : "memory", "m0");
 }
 
 // One operand of one tile: BM rows of i (or j).  Wave w issues its loads q = 0 .. LQ-1 of every stage; fragments
@@ -587,7 +604,8 @@ struct TileKernel {
         constexpr int r = rc, e = r / (WJ * NI), j = r % (WJ * NI) / NI, i = r % NI;
         constexpr int l0 = spread_lo(r, NQ, R), l1 = spread_hi(r, NQ, R);
         if constexpr (l0 == 0 && l1 > 0) feed.begin_stage();
-        if constexpr (l1 > l0) tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i], feed.template load<l0>(cbuf));
+        constexpr bool first = l0 == 0 || l0 == OpA::LQ;
+        if constexpr (l1 > l0) tile_mfma<e, first>(acc[j][i], fb[h][j], fa[h][i], feed.template load<l0>(cbuf));
         else tile_mfma<e>(acc[j][i], fb[h][j], fa[h][i]);
         static_for<(l1 > l0 ? l1 - l0 - 1 : 0)>([&](auto Lc) { load_now(feed.template load<l0 + 1 + Lc>(cbuf)); });
         if constexpr (l1 > l0 && l1 == NQ) feed.end_stage();
