@@ -23,8 +23,9 @@ def quantize_weights(w: torch.Tensor):
 
 class MoeInt8Layer:
     """`w_gate_up` [E, 2I, H] (gate rows, then up rows) and `w_down` [E, H, I] are quantized here; the router stays in
-    its own type.  All buffers are allocated once for batches of up to max_T tokens (a larger batch allocates more; graphs
-    captured before keep theirs), so one forward runs at a time."""
+    its own type.  All buffers are allocated once for batches of up to max_T tokens, so one forward runs at a time.  A
+    larger batch replaces them by ones of at least twice the size, or of its own size where memory does not suffice; the
+    old ones go, unless a graph was captured with them (those that stay, together, are about as large as the last)."""
 
     def __init__(self, w_router, bias, w_gate_up, w_down, k, max_T=1):
         self.w_router, self.bias, self.k = w_router, bias, k
@@ -35,7 +36,9 @@ class MoeInt8Layer:
             raise ValueError("w_router %s: [%d, %d] expected" % (tuple(w_router.shape), self.E, self.H))
         if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (self.E,)):
             raise ValueError("bias %s %s: float32 [%d] expected" % (bias.dtype, tuple(bias.shape), self.E))
-        self._outgrown = []
+        self._outgrown = []  # buffers whose addresses captured graphs hold
+        self._captured, self._stream = False, None  # of the present buffers: a graph holds them; the stream of the last forward
+        self._sized_T, self._rws_bytes = 0, 256  # workspace that routes any batch of up to _sized_T tokens
         self.gate_up = quantize_weights(w_gate_up)
         self.down = quantize_weights(w_down)
         self._alloc(max_T)
@@ -52,8 +55,24 @@ class MoeInt8Layer:
         self.h, self.h_scale = torch.empty((n, I), dtype=torch.int8, device=d), torch.empty(n, **f32)
         self.y = torch.empty((n, H), **f32)
         xdt = "f32" if self.w_router.dtype == torch.float32 else "bf16"
-        rws = max(api.moe_route_permute_workspace(t, H, E, k, xdt) for t in range(1, T + 1))
-        self.rws = torch.empty(max(rws, 256), dtype=torch.uint8, device=d)
+        for t in range(self._sized_T + 1, T + 1):
+            self._rws_bytes = max(self._rws_bytes, api.moe_route_permute_workspace(t, H, E, k, xdt))
+        self._sized_T = max(self._sized_T, T)
+        self.rws = torch.empty(self._rws_bytes, dtype=torch.uint8, device=d)
+
+    def _grow(self, T):
+        old = (self.ids, self.gates, self.counts, self.offsets, self.perm, self.inv, self.q, self.q_scale, self.gu, self.h,
+               self.h_scale, self.y, self.rws)
+        try:
+            self._alloc(max(T, 2 * self.max_T))
+        except torch.cuda.OutOfMemoryError:
+            self._alloc(T)
+        if self._captured:
+            self._outgrown.append(old)
+        elif self._stream is not None:
+            for t in old:  # the last forward may still run, on another stream than the one they were allocated on
+                t.record_stream(self._stream)
+        self._captured, self._stream = False, None
 
     def forward(self, x, out=None):
         """One layer forward on the current stream (x [T, H] in the router's type)."""
@@ -67,12 +86,12 @@ class MoeInt8Layer:
         elif out.shape != x.shape or out.device != x.device:
             raise ValueError("out %s on %s: that of x expected" % (tuple(out.shape), out.device))
         if T > self.max_T:
-            self._outgrown.append((self.ids, self.gates, self.counts, self.offsets, self.perm, self.inv, self.q,
-                                   self.q_scale, self.gu, self.h, self.h_scale, self.y, self.rws))
-            self._alloc(T)
+            self._grow(T)
         if T == 0:
             return out
         with torch.cuda.device(x.device):
+            self._stream = torch.cuda.current_stream()
+            self._captured = self._captured or torch.cuda.is_current_stream_capturing()
             self._run(x, out, T)
         return out
 
