@@ -43,26 +43,26 @@ class MoeInt8Layer:
         self.down = quantize_weights(w_down)
         self._alloc(max_T)
 
+    # the buffers, in the order _alloc makes them
+    _BUFFERS = ("ids", "gates", "counts", "offsets", "perm", "inv", "q", "q_scale", "gu", "h", "h_scale", "y", "rws")
+
     def _alloc(self, T):
+        """All buffers for T tokens, or, if one cannot be had, none of them: the layer stays as it was."""
         d, k, H, I, E = self.w_router.device, self.k, self.H, self.I, self.E
-        self.max_T, n = T, max(T * k, 1)
-        i32, f32 = dict(dtype=torch.int32, device=d), dict(dtype=torch.float32, device=d)
-        self.ids, self.gates = torch.empty((T, k), **i32), torch.empty((T, k), **f32)
-        self.counts, self.offsets = torch.empty(E, **i32), torch.empty(E + 1, **i32)
-        self.perm, self.inv = torch.empty(n, **i32), torch.empty(n, **i32)
-        self.q, self.q_scale = torch.empty((T, H), dtype=torch.int8, device=d), torch.empty(T, **f32)
-        self.gu = torch.empty((n, 2 * I), dtype=torch.bfloat16, device=d)
-        self.h, self.h_scale = torch.empty((n, I), dtype=torch.int8, device=d), torch.empty(n, **f32)
-        self.y = torch.empty((n, H), **f32)
+        n, sized_T, rws_bytes = max(T * k, 1), self._sized_T, self._rws_bytes
         xdt = "f32" if self.w_router.dtype == torch.float32 else "bf16"
-        for t in range(self._sized_T + 1, T + 1):
-            self._rws_bytes = max(self._rws_bytes, api.moe_route_permute_workspace(t, H, E, k, xdt))
-        self._sized_T = max(self._sized_T, T)
-        self.rws = torch.empty(self._rws_bytes, dtype=torch.uint8, device=d)
+        for t in range(sized_T + 1, T + 1):
+            rws_bytes = max(rws_bytes, api.moe_route_permute_workspace(t, H, E, k, xdt))
+        i8, i32, f32, u8 = torch.int8, torch.int32, torch.float32, torch.uint8
+        sizes = (((T, k), i32), ((T, k), f32), ((E,), i32), ((E + 1,), i32), ((n,), i32), ((n,), i32), ((T, H), i8),
+                 ((T,), f32), ((n, 2 * I), torch.bfloat16), ((n, I), i8), ((n,), f32), ((n, H), f32), ((rws_bytes,), u8))
+        made = [torch.empty(shape, dtype=dtype, device=d) for shape, dtype in sizes]
+        for name, t in zip(self._BUFFERS, made):
+            setattr(self, name, t)
+        self.max_T, self._sized_T, self._rws_bytes = T, max(sized_T, T), rws_bytes
 
     def _grow(self, T):
-        old = (self.ids, self.gates, self.counts, self.offsets, self.perm, self.inv, self.q, self.q_scale, self.gu, self.h,
-               self.h_scale, self.y, self.rws)
+        old = [getattr(self, name) for name in self._BUFFERS]
         try:
             self._alloc(max(T, 2 * self.max_T))
         except torch.cuda.OutOfMemoryError:

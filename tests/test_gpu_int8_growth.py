@@ -120,3 +120,48 @@ def test_growth_while_the_last_forward_runs_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and torch.equal(more_out, more_ref)
         assert all(bool((j == 3).all()) for j in junk)
+
+
+@pytest.mark.parametrize("after", range(13))
+def test_a_growth_that_fails_leaves_the_layer_as_it_was(monkeypatch, after):
+    """Memory runs out at any of the buffers: the layer must not take itself for a larger one (its kernels would write
+    past buffers of the old size), and serves batches of the old size, and larger ones once there is memory."""
+    T, n = 6, 40
+    x, ref, small = tokens(n), layer_of(n).forward(tokens(n)), layer_of(T).forward(tokens(n)[:T])
+    layer, empty, made = layer_of(T), torch.empty, []
+    out = torch.empty_like(x)
+
+    def scarce(*a, **kw):
+        if len(made) % 13 == after:
+            made.clear()
+            raise torch.cuda.OutOfMemoryError("out of memory")
+        made.append(1)
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", scarce)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        layer.forward(x, out)
+    monkeypatch.undo()
+    assert layer.max_T == T
+    for name in ("ids", "gates", "q", "q_scale"):
+        assert getattr(layer, name).shape[0] == T, name
+    for name in ("perm", "inv", "gu", "h", "h_scale", "y"):
+        assert getattr(layer, name).shape[0] == T * k, name
+    assert torch.equal(layer.forward(x[:T]), small)
+    assert torch.equal(layer.forward(x), ref)
+
+
+def test_memory_for_the_batch_but_not_for_twice_the_old_size(monkeypatch):
+    T = 6
+    x, ref, empty = tokens(T + 1), layer_of(T + 1).forward(tokens(T + 1)), torch.empty
+    layer = layer_of(T)
+
+    def scarce(*a, **kw):
+        if a[0] == (2 * T, k):
+            raise torch.cuda.OutOfMemoryError("out of memory")
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", scarce)
+    got = layer.forward(x)
+    monkeypatch.undo()
+    assert layer.max_T == T + 1 and torch.equal(got, ref)
