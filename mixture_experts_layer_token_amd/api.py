@@ -227,12 +227,19 @@ def _step(t, dim):
     return step
 
 
+def _check_stream(stream, dev):
+    """A launch runs on its stream's device, where the addresses of tensors on another one mean nothing."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("tensors on device %d, stream on device %d" % (dev, stream.device_index))
+
+
 def _launch(f, args, tensors, stream):
     """Call f(*args, stream) on the device that holds the tensors, whichever is current."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors on devices %d and %d" % (dev, t.get_device()))
+    _check_stream(stream, dev)
     if stream is not None:
         s = stream.cuda_stream
     else:
@@ -268,6 +275,7 @@ def _same_dt(a, b):
 
 
 def _grouped_ws(ws, dt, g, device, stream):
+    _check_stream(stream, device.index)
     if ws is None:
         need = int(lib().moe_grouped_workspace(dt, g.rows, g.N, g.K, g.E))
         if need:
