@@ -8,20 +8,29 @@ namespace moe {
 namespace {
 
 // How many parts the rows of each group are cut into for a weight gradient: its tiles of 128 x 128 alone would leave
-// compute units idle.  A part keeps at least 256 rows, and two parts share a compute unit at most.  fp32 parts are bound by
-// the matrix cores, so two on one unit take twice as long as one and the units with one wait: of the counts that keep the
-// busiest unit's share of the rows smallest, the least.  (128 x 2880 over 4096 rows, 23 tiles: in 16 parts each 48 us, in
-// 11 41; 384 x 7168, 168 tiles: whole 248 us, in 3 parts 187.)  bf16 parts wait on memory and take all that fit.
-int dw_split(int type, int rows, int N, int K, int E) {
+// compute units idle.  A part keeps at least 256 rows.
+//  - bf16, direct loads: one workgroup to a compute unit (four stages in LDS), 0.5 us per stage of 64 rows and 8 to begin and
+//    end; the parts' sum takes 5 us and its bytes at 4.5 TB/s.  The count that takes the least, measured: 640 x 640 over
+//    8 groups of 1024 rows (200 tiles) whole 15 us, in 2 parts 32; over 4 groups 13 and 22; 1024 x 1024 over 8192 rows (64
+//    tiles) whole 57, in 4 parts 29, in 8 38; 1280 x 1280 (100 tiles) whole 58, in 2 parts 41, in 5 48.
+//  - bf16 through registers (staged): two workgroups to a unit, waiting on memory: all that fit.  1023 x 1023 over 8192 rows
+//    whole 229 us, in 4 parts 74, in 8 58; 2047 x 1535 (192 tiles) whole 229, in 2 parts 143.
+//  - fp32 is bound by the matrix cores, so two parts on one unit take twice as long as one and the units with one wait: of the
+//    counts that keep the busiest unit's share of the rows smallest, the least.  128 x 2880 over 4096 rows, 23 tiles: in 16
+//    parts each 48 us, in 11 41; 384 x 7168, 168 tiles: whole 248 us, in 3 parts 187.
+int dw_split(int type, bool staged, int rows, int N, int K, int E) {
   const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
   if (tiles >= 256) return 1;
   const long long by_rows = (long long)rows / E / 256, by_tiles = 512 / tiles;
-  const int most = (int)(by_rows < by_tiles ? by_rows : by_tiles);
-  if (type != kF32) return most < 2 ? 1 : most > 32 ? 32 : most;
-  int best = 1, share = 1;  // the busiest unit holds share parts of best
-  for (int s = 2; s <= most && s <= 32; s++) {
-    const int n = (int)((tiles * s + 255) / 256);
-    if (n * best < share * s) best = s, share = n;
+  const int most = (int)std::min({by_rows, by_tiles, 32LL});
+  if (type != kF32 && staged) return std::max(most, 1);
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= most || s == 1; s++) {
+    const double turns = (double)((tiles * s + 255) / 256), stages = (double)rows / E / 64 / s;  // of the busiest unit
+    const double sum = s > 1 ? 5 + 8.0 * s * E * N * K / 4.5e6 : 0;
+    const double cost = type == kF32 ? turns / s : turns * (0.5 * stages + 8) + sum;
+    if (cost < least) best = s, least = cost;
   }
   return best;
 }
@@ -59,7 +68,8 @@ TileShape cheapest_shape(const GroupArgs& a, int op, int eb, double large, doubl
 }  // namespace
 
 size_t grouped_workspace(int type, int rows, int N, int K, int E) {
-  const int s = dw_split(type, rows, N, K, E);
+  // (whether operands start on 16 bytes is not known here: the more parts of the two)
+  const int s = std::max(dw_split(type, true, rows, N, K, E), dw_split(type, false, rows, N, K, E));
   return s > 1 ? ((size_t)s * E * N * K * 4 + 255) / 256 * 256 : 0;
 }
 
@@ -82,7 +92,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
       return launch_grouped_decode(a, type, t == kLarge, s);
   }
   if (op == kOpDw) {
-    const int split = dw_split(type, a.rows, a.N, a.K, a.E);
+    const int split = dw_split(type, t == kStaged, a.rows, a.N, a.K, a.E);
     if (split > 1) {
       if (t == kLarge) t = kDeep;
       GroupArgs p = a;

@@ -60,6 +60,23 @@ def test_gathered_weight_gradient_in_parts(counts, N, K, k, layout, dt):
         R.assert_product(dw, *reference_on_gpu("dw", xg, None, dy, off), what="dw")
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K,aligned", [([1024] * 8, 640, 640, True), ([1024] * 8, 640, 640, False),
+                                                ([8192], 1920, 1536, True)])
+def test_weight_gradient_whose_tiles_fill_the_card_is_summed_in_one(counts, N, K, aligned, dt):
+    """180 to 200 tiles: with one workgroup to a compute unit two parts each would take two rounds of half the length.  Rows
+    on no 16-byte boundary go two to a unit, and bf16 ones are cut."""
+    off, E, rows = R.offsets_of(counts), len(counts), sum(counts)
+    _, x = rows_tensor((rows, K), dt, "dense" if aligned else "shifted", gen(44))
+    _, dy = rows_tensor((rows, N), dt, "dense", gen(45))
+    need, ws = nan_workspace(dt, rows, N, K, E)
+    dw = torch.empty((E, N, K), device="cuda")
+    moe.moe_grouped_gemm_dw(dy, x, torch.from_numpy(off).cuda(), dw, ws=ws)
+    torch.cuda.synchronize()
+    R.assert_product(dw, *reference_on_gpu("dw", x, None, dy, off), what="dw")
+    assert bool((ws == 0xFF).all()) == (aligned or dt == torch.float32)
+
+
 # ------------------------------------------------------------------ expert strides
 def spread(E, N, K, pad, dt, fill):
     """[E, N, K] view of a buffer with `pad` elements between experts, and the buffer."""
