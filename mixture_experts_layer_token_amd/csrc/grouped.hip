@@ -47,6 +47,26 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   store_out(dw, (size_t)(e * w_stride + (row - e * N) * ldw + (i - row * K)), v, bf16);
 }
 
+// Whether a forward product runs on the kernel that spreads every expert's features over N / 16 workgroups.  It wins while
+// the tile kernel would have too few tiles of 128 x 128 to fill the card, but reads all rows of x again for every 16 features,
+// so fewer tiles are allowed the more rows there are.  Measured, this kernel against the tile kernel (us, weights not in a
+// cache; "rows" per touched expert):
+//   bf16   5760 x 2880, 1 expert (45 tiles): 1 row 15 : 23, 32 rows 24 : 25, 48 rows 30 : 26
+//          2880 x 2880, 1 row: 8 experts (184 tiles) 31 : 45, 16 experts (368) 56 : 53;  4 experts (92): 4 rows 24 : 24, 16 28 : 25
+//          4096 x 7168, 8 experts (256): 1 row 85 : 115;  4096 x 14336, 8 experts (256): 4 rows 173 : 163, 32 rows 364 : 168
+//          4096 x 4096, 1 expert (32): 64 rows 25 : 34
+//   int8   5760 x 2880, 45 tiles: 32 rows 15 : 19, 64 rows 21.5 : 20.8;  4096 x 14336, 256 tiles: 1 row 81 : 81, 32 rows 184 : 83
+//   rows through registers (staged), bf16   5759 x 2881 (45): 32 rows 86 : 86, 48 rows 102 : 89;  2879 x 2881, 4 experts (92):
+//          1 row 71 : 83, 8 rows 91 : 84;  4095 x 4097, 8 experts (256): 1 row 159 : 119, 32 rows 386 : 124
+//   fp32 (bound by the matrix cores, of which its many workgroups use more at a time)   4096 x 14336, 8 experts (256):
+//          8 rows 387 : 466, 16 rows 490 : 466;  14336 x 4096, 1 expert (112): 48 rows 138 : 145, 64 rows 166 : 146
+bool few_rows_kernel(int type, bool staged, int rows, int N, int E) {
+  const long long tiles = (long long)std::min(rows, E) * ((N + 127) / 128), mean = ((long long)rows + E - 1) / E;
+  if (mean > kDecodeRows) return false;
+  if (type == kF32) return tiles * (mean + 16) <= 7500;
+  return tiles * (mean + (staged ? 16 : 4)) <= 2200;
+}
+
 // The tile shape that takes the least time, from rounds of tiles and stages of 128 bytes (us; fitted to measured calls).
 // A 256 x 256 tile has a compute unit to itself: 1.46 per stage of full tiles, 10 to begin and end; 128 x 128 ones go two
 // to a compute unit, 0.94 and 7; where they leave units idle anyway, four stages in LDS instead of two hide the loads
@@ -85,10 +105,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   const bool ay = op == kOpY || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
   TileShape t = ax && aw && ay && tile_spans_fit(a, op, eb) ? kLarge : kStaged;
   if (op == kOpY) {
-    // few rows and few tiles: the kernel that spreads each expert's features over N / 16 workgroups
-    const long long groups = a.rows < a.E ? a.rows : a.E;
-    const long long mean = (a.rows + a.E - 1) / a.E, few = groups * ((a.N + 127) / 128);
-    if ((mean <= 32 && few < 512) || (mean <= 64 && few < 64))
+    if (few_rows_kernel(type, t == kStaged, a.rows, a.N, a.E))
       return launch_grouped_decode(a, type, t == kLarge, s);
   }
   if (op == kOpDw) {

@@ -135,6 +135,7 @@ int launch_tile_dx_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_dw_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_dw_bf16_gather(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_f32(const GroupArgs& a, int op, TileShape t, hipStream_t s);
+constexpr int kDecodeRows = 64;  // rows of a workgroup there
 // grouped_decode.hip: forward for few rows; direct: rows on 16-byte boundaries and spans that fit
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s);
 // the kernel that suits the call; ws holds grouped_workspace bytes

@@ -25,7 +25,7 @@ __device__ __forceinline__ f32x4 mma(const f32x4& b, const f32x4& a, f32x4 c) {
   return c;
 }
 
-constexpr int kDecodeRows = 64, kDecodeCols = 16;
+constexpr int kDecodeCols = 16;
 
 // Rows of 16 bytes per lane, at byte c of the row: through a buffer descriptor (DIRECT), whose end turns everything
 // outside into zeros, or by ordinary loads at any address.
