@@ -381,7 +381,8 @@ typedef struct {
 } moe_grouped;
 
 /* Workspace bytes the three products below need (device, 256-byte aligned; the largest of the three,
- * 0 when none): partial sums of weight gradients with few tiles.  One call at a time may use it. */
+ * 0 when none): partial sums of weight gradients with few tiles.  The other two ask for it as well, so that one buffer
+ * serves all three, but do not write to it now.  One call at a time may use it. */
 size_t moe_grouped_workspace(int dt, int rows, int N, int K, int E);
 
 /*

@@ -131,6 +131,8 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     const double ni = op == kOpDw ? (double)((a.N + b - 1) / b) : a.E == 1 ? (double)((a.rows + b - 1) / b) : std::max(1.0, avg / b + 0.5);
     return ni * a.E * ((nj + b - 1) / b);
   };
+  // (fp32 has tiles of 128 x 128 only, with two stages, whatever shape is chosen: the order below by the chosen shape's tiles or
+  // by its own took the same time to 1%)
   if (t == kLarge) t = cheapest_shape(a, op, eb, tiles(256), tiles(128), op == kOpDw ? 256 : std::min(avg, 256.0));
   // Groups of many tiles are shared out over the XCDs one by one, as they may differ in cost (weight gradients of 8
   // experts with 540 to 1000 rows 1228 -> 906 us); small ones stay on one XCD, whose L2 then holds their rows (16384 rows over 16

@@ -81,9 +81,9 @@ __device__ __forceinline__ float gate_exact(float g, float u) { return g / (1.f 
 
 // q = the integer nearest to 127 v / max, halves to even.  v and max are scaled by 2^e, which puts max into
 // [1, 2) (so that neither the product nor the reciprocal leaves the fp32 range; an element this pushes into
-// the denormals is 0 anyway).  The quotient by reciprocal is off by less than 2^-16: only next to a half is
-// it taken again, in 64 bits, where 127 v is exact and the quotient is off by 2^-45 -- closer to a half than that
-// without meeting it no two fp32 numbers' ratio comes.
+// the denormals is 0 anyway).  The quotient by reciprocal is off by less than 2^-15.4 (three roundings of 2^-24 each, at
+// values up to 127): only within 2^-15 of a half is it taken again, in 64 bits, where 127 v is exact and the quotient is off
+// by 2^-45 -- closer to a half than that without meeting it no two fp32 numbers' ratio comes.
 __device__ __forceinline__ int quantize(float v, int e, float top, float inv) {
   const float x = 127.f * ldexpf(v, e);
   const float t = x * inv;

@@ -3,7 +3,9 @@ activations quantized on the way with a scale per token.
 
 The experts take half the bytes of bf16 ones.  Forward: moe_route_permute on the bf16 (or fp32) tokens, moe_quant_rows
 (each token once, before it is gathered), moe_grouped_gemm_i8 (gate/up), moe_quant_rows with the SwiGLU gate (the
-gated rows exist in 8 bits only), moe_grouped_gemm_i8 (down, fp32 results), moe_combine.
+gated rows exist in 8 bits only), moe_grouped_gemm_i8 (down, fp32 results), moe_combine.  The gate/up results are kept in
+bf16 whatever the tokens' type: that rounds each value by at most 2^-8 of it, the 8-bit rounding of the gated rows that
+follows by 2^-8 of the row's largest.
 """
 from __future__ import annotations
 
