@@ -402,6 +402,27 @@ int moe_grouped_gemm_dx(const moe_grouped* g, int dt, const void* dy, const void
 int moe_grouped_gemm_dw(const moe_grouped* g, int dt, const void* dy, const void* x, void* dw, int dwdt, void* ws,
                         size_t ws_bytes, void* stream);
 
+/*
+ * The gated feed-forward block up to its down matrix, and the gradient that reaches its projections from behind it, each in
+ * one kernel: both projections, the activation and the product.  s(z) = 1 / (1 + e^-z):
+ *   moe_grouped_swiglu     [g | u][p] = w[e] x[r(p)],  h[p] = g s(g) u
+ *   moe_grouped_swiglu_dx  dh[p] = w[e]^T dy[p],  dgu[p] = [dh u s(g) (1 + g (1 - s(g))) | dh g s(g)],  h[p] = g s(g) u
+ * As moe_grouped_gemm then moe_swiglu, and moe_grouped_gemm_dx then moe_swiglu_grad, but nothing between them is rounded or
+ * written: h comes from the fp32 sums g and u (from the rounded ones in the gradient, which is what it reads), and dh stays
+ * in fp32.  The block's other gradients are grouped products: moe_grouped_gemm_dx and _dw of dgu, _dw of dy and h.  With
+ * E = 1 and offsets {0, rows} they are one dense block.
+ *   moe_grouped_swiglu: N = I; x device [x_rows or rows][K], w device [E][2I][K] (I gate rows, then I up rows; w_stride 0:
+ *     2 * N * (ldw or K)), h device [rows][I] (ldy between its rows), gu device [rows][2I] contiguous (out), or NULL: not kept
+ *   moe_grouped_swiglu_dx: N = H, K = I of the down matrix; dy device [rows][H], w device [E][H][I], gu device [rows][2I],
+ *     dgu device [rows][2I] (out) and h device [rows][I] (out, or NULL), all three contiguous; perm_src, x_rows and ldx are
+ *     ignored
+ * Everything has the type dt.  Rows at and past offsets[E] are left as they were; results must not overlap operands.
+ * Errors: as moe_grouped_gemm; no workspace.
+ */
+int moe_grouped_swiglu(const moe_grouped* g, int dt, const void* x, const void* w, void* h, void* gu, void* stream);
+int moe_grouped_swiglu_dx(const moe_grouped* g, int dt, const void* dy, const void* w, const void* gu, void* dgu,
+                          void* h, void* stream);
+
 /* ------------------------------------------- 8-bit integer experts (W8A8) */
 
 /* what moe_quant_rows does to a row before it is quantized */
@@ -451,6 +472,63 @@ int moe_grouped_gemm_i8(const moe_grouped* g, const int8_t* q, const float* q_sc
 int moe_swiglu(const void* gu, int dt, int rows, int I, const int32_t* n_rows, void* h, void* stream);
 int moe_swiglu_grad(const void* gu, const void* dh, int dt, int rows, int I, const int32_t* n_rows, void* dgu,
                     void* h, void* stream);
+
+/* ------------------------------------------------------------ norm of rows */
+
+/*
+ * Layer norm (rms 0) or RMS norm (rms 1) of rows, and its gradient:
+ *   mean = sum_j x[j] / H (RMS: 0),  rstd = 1 / sqrt(sum_j (x[j] - mean)^2 / H + eps),  xh = (x - mean) rstd
+ *   moe_norm       y = xh weight + bias,  stats[r] = {mean, rstd} unless NULL
+ *   moe_norm_grad  v = dy weight,  dx = rstd (v - sum v / H (RMS: 0) - xh sum(v xh) / H) (+ add[r] unless NULL: the
+ *                  residual's gradient),  dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * fp32 arithmetic, one rounding of each result; no atomics: results are bitwise reproducible.
+ *   x, y, dy, dx, add device [rows][H] of type dt (ldx between rows of x, ldy between those of y or dy; dx and add contiguous);
+ *   weight, bias, dweight, dbias device [H] of type pdt; weight NULL: ones, bias NULL: zeros; dweight or dbias NULL: not
+ *   asked for (zeros where there are no rows); stats device [rows][2] fp32
+ * A row that holds a NaN or an infinity spoils its own results and the sums over rows, no other row.  add may be dx;
+ * results must not overlap operands otherwise.
+ * Errors: MOE_ERR_INVALID (null pointers, bad types, sizes, strides or eps, pointers that are not element-aligned),
+ * MOE_ERR_WORKSPACE (the gradient: moe_norm_workspace bytes, device, 256-byte aligned; one call at a time may use it).
+ */
+typedef struct {
+  int rows, H;       /* 0..1<<24, 1..1<<20 */
+  int rms;           /* 0 or 1 */
+  int dt, pdt;       /* type of the rows; of weight and bias and of their gradients */
+  float eps;         /* >= 0 (the gradient reads rstd from stats instead) */
+  int64_t ldx, ldy;  /* elements between rows; 0: contiguous */
+} moe_norm_desc;
+
+int moe_norm(const moe_norm_desc* d, const void* x, const void* weight, const void* bias, void* y, float* stats,
+             void* stream);
+size_t moe_norm_workspace(int rows, int H);
+int moe_norm_grad(const moe_norm_desc* d, const void* dy, const void* x, const void* weight, const float* stats,
+                  const void* add, void* dx, void* dweight, void* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------- gradient norm, clipping */
+
+/*
+ * The 2-norm over all elements of a list of gradients, and clipping by it:
+ *   moe_grad_norm       norm = sqrt(sum over tensors and elements of src^2)
+ *   moe_clip_grad_norm  and dst = src min(1, max_norm / norm), rounded once, for every tensor whose dst is not NULL
+ * Squares and their sum are held in 64 bits; the order of the sum is fixed (bitwise reproducible, no atomics).  norm is rounded
+ * to fp32.  A norm that is not finite is reported and scales nothing: dst = src.
+ *   t     host, n entries, read during the call only (it may be captured into a graph: the addresses are then fixed)
+ *   norm  device, one fp32 (out)
+ *   ws    moe_grad_norm_workspace bytes (device, 256-byte aligned); one call at a time may use it
+ * dst may be src.  A dst that overlaps anything else in the list is refused, a gradient named twice in place among them.
+ * Errors: MOE_ERR_INVALID (n out of 0..1<<16, null or misaligned pointers, bad types, numel out of 0..1<<40, overlaps,
+ * max_norm not positive and finite), MOE_ERR_WORKSPACE.
+ */
+typedef struct {
+  const void* src;  /* device, numel contiguous elements */
+  void* dst;        /* device, same type; NULL: only counted (moe_grad_norm ignores it) */
+  int64_t numel;
+  int dt;
+} moe_tensor;
+
+size_t moe_grad_norm_workspace(const moe_tensor* t, int n);
+int moe_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, size_t ws_bytes, void* stream);
+int moe_clip_grad_norm(const moe_tensor* t, int n, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ combine */
 

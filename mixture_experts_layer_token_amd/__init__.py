@@ -12,6 +12,8 @@ from .api import (DT, FMT, ExpertCache, experts_desc, moe_combine, moe_compress_
                   moe_route, moe_route_permute, moe_route_permute_workspace)
 from .api import (moe_combine_grad, moe_grouped_gemm, moe_grouped_gemm_dw, moe_grouped_gemm_dx, moe_grouped_gemm_i8,
                   moe_grouped_workspace, moe_quant_rows, moe_swiglu, moe_swiglu_grad)
+from .api import (moe_clip_grad_norm, moe_grad_norm, moe_grad_norm_workspace, moe_grouped_swiglu, moe_grouped_swiglu_dx,
+                  moe_norm, moe_norm_grad, moe_norm_workspace)
 from ._lib import MoeError, header_symbols, lib
 
 __all__ = ["DT", "FMT", "ExpertCache", "experts_desc", "moe_combine", "moe_compress_bound", "moe_compress_package",
@@ -19,4 +21,6 @@ __all__ = ["DT", "FMT", "ExpertCache", "experts_desc", "moe_combine", "moe_compr
            "moe_ffn_workspace", "moe_pack_expert", "moe_package_bytes", "moe_permute", "moe_permute_workspace",
            "moe_route", "moe_route_permute", "moe_route_permute_workspace", "moe_combine_grad", "moe_grouped_gemm",
            "moe_grouped_gemm_dw", "moe_grouped_gemm_dx", "moe_grouped_gemm_i8", "moe_grouped_workspace",
-           "moe_quant_rows", "moe_swiglu", "moe_swiglu_grad", "MoeError", "header_symbols", "lib"]
+           "moe_quant_rows", "moe_swiglu", "moe_swiglu_grad", "moe_clip_grad_norm", "moe_grad_norm",
+           "moe_grad_norm_workspace", "moe_grouped_swiglu", "moe_grouped_swiglu_dx", "moe_norm", "moe_norm_grad",
+           "moe_norm_workspace", "MoeError", "header_symbols", "lib"]

@@ -27,6 +27,15 @@ class MoeGrouped(ctypes.Structure):
                 ("ldw", ctypes.c_int64), ("w_stride", ctypes.c_int64)]
 
 
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("rows", c_int), ("H", c_int), ("rms", c_int), ("dt", c_int), ("pdt", c_int), ("eps", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("src", vp), ("dst", vp), ("numel", ctypes.c_int64), ("dt", c_int)]
+
+
 # moe_copy_fn: int (*)(void* ctx, void* dst, const void* src, size_t bytes, void* stream)
 COPY_FN = ctypes.CFUNCTYPE(c_int, vp, vp, vp, c_size_t, vp)
 
@@ -77,10 +86,18 @@ SIGNATURES = {
     "moe_grouped_gemm": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
     "moe_grouped_gemm_dx": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
     "moe_grouped_gemm_dw": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, c_int, vp, c_size_t, vp], c_int),
+    "moe_grouped_swiglu": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, vp, vp], c_int),
+    "moe_grouped_swiglu_dx": ([ctypes.POINTER(MoeGrouped), c_int, vp, vp, vp, vp, vp, vp], c_int),
     "moe_grouped_gemm_i8": ([ctypes.POINTER(MoeGrouped), vp, f32p, vp, f32p, vp, c_int, vp], c_int),
     "moe_quant_rows": ([vp, c_int, c_int, c_int, c_int, i32p, vp, f32p, vp], c_int),
     "moe_swiglu": ([vp, c_int, c_int, c_int, i32p, vp, vp], c_int),
     "moe_swiglu_grad": ([vp, vp, c_int, c_int, c_int, i32p, vp, vp, vp], c_int),
+    "moe_norm": ([ctypes.POINTER(MoeNormDesc), vp, vp, vp, vp, f32p, vp], c_int),
+    "moe_norm_workspace": ([c_int, c_int], c_size_t),
+    "moe_norm_grad": ([ctypes.POINTER(MoeNormDesc), vp, vp, vp, f32p, vp, vp, vp, vp, vp, c_size_t, vp], c_int),
+    "moe_grad_norm_workspace": ([vp, c_int], c_size_t),  # (moe_tensor lists: any buffer of that layout)
+    "moe_grad_norm": ([vp, c_int, f32p, vp, c_size_t, vp], c_int),
+    "moe_clip_grad_norm": ([vp, c_int, ctypes.c_float, f32p, vp, c_size_t, vp], c_int),
     "moe_combine_grad": ([vp, c_int, f32p, f32p, i32p, c_int, c_int, c_int, vp, c_int, f32p, i32p, c_int, f32p, vp],
                          c_int),
     "moe_combine": ([f32p, f32p, i32p, c_int, c_int, c_int, f32p, vp, c_int, vp], c_int),

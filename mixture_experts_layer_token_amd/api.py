@@ -7,12 +7,13 @@ library's HIP kernels.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 
 import numpy as np
 import torch
 
-from ._lib import COPY_FN, MoeCacheDesc, MoeCachePlan, MoeCacheStats, MoeExperts, MoeGrouped, check, lib
+from ._lib import COPY_FN, MoeCacheDesc, MoeCachePlan, MoeCacheStats, MoeExperts, MoeGrouped, MoeNormDesc, check, lib
 
 FMT = {"f32": 0, "bf16": 1, "mxfp4": 2, "int4g32": 3}
 DT = {"f32": 0, "bf16": 1}
@@ -311,6 +312,36 @@ def moe_grouped_gemm_dw(dy, x, offsets, dw, perm_src=None, k=1, ws=None, stream=
             (dy, x, dw, offsets, perm_src, ws), stream)
 
 
+def moe_grouped_swiglu(x, w, offsets, h, gu=None, perm_src=None, k=1, stream=None):
+    """h[p] = SiLU(g) * u with [g | u] = w[e] x[r(p)] for the rows p of every expert e, in one kernel: w [E, 2I, K] (gate
+    rows, then up rows) -> h [rows, I]; `gu`: optional [rows, 2I] that takes [g | u] for the backward pass."""
+    if w.dim() != 3 or w.shape[1] % 2:
+        raise ValueError("w: [E, 2I, K] expected, got %s" % (tuple(w.shape),))
+    I = w.shape[1] // 2
+    g, dt = _grouped(x, w[:, :I], h, offsets, perm_src, k), _same_dt(x, w)
+    g.ldw = _step(w, 1)  # (of one gate row alone there is no step)
+    _need(h, x.dtype, (h.shape[0], I), "h")
+    if gu is not None:
+        _need(gu, x.dtype, (h.shape[0], 2 * I), "gu")
+    _launch(lib().moe_grouped_swiglu, (ctypes.byref(g), dt, _rowp(x), _rowp(w), _rowp(h), _ptr(gu)),
+            (x, w, h, gu, offsets, perm_src), stream)
+
+
+def moe_grouped_swiglu_dx(dy, w, gu, offsets, dgu, h=None, stream=None):
+    """The gradient of [g | u] from that of the rows behind the down matrices w [E, H, I], in one kernel: dgu [rows, 2I] from
+    dy [rows, H] and gu [rows, 2I]; `h`: optional [rows, I] that takes SiLU(g) * u again."""
+    if w.dim() != 3:
+        raise ValueError("w: [E, H, I] expected, got %s" % (tuple(w.shape),))
+    rows, I = dy.shape[0], w.shape[2]
+    _need(dgu, dy.dtype, (rows, 2 * I), "dgu")
+    _need(gu, dy.dtype, (rows, 2 * I), "gu")
+    if h is not None:
+        _need(h, dy.dtype, (rows, I), "h")
+    g, dt = _grouped(dgu[:, :I], w, dy, offsets, None, 1), _same_dt(dy, w)
+    _launch(lib().moe_grouped_swiglu_dx,
+            (ctypes.byref(g), dt, _rowp(dy), _rowp(w), _ptr(gu), _ptr(dgu), _ptr(h)), (dy, w, gu, dgu, h, offsets), stream)
+
+
 def _need(t, dtype, shape, what):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
         raise ValueError("%s: %s %s expected, got %s %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
@@ -362,6 +393,113 @@ def moe_swiglu_grad(gu, dh, dgu, h=None, n_rows=None, stream=None):
         _need(h, dh.dtype, (rows, I), "h")
     _launch(lib().moe_swiglu_grad, (_ptr(gu), _ptr(dh), _dt(gu), rows, I, _n_rows(n_rows), _ptr(dgu), _ptr(h)),
             (gu, dh, dgu, h, n_rows), stream)
+
+
+def _norm_desc(x, y, params, eps, rms) -> MoeNormDesc:
+    """Descriptor of a norm of rows; params: weight, bias and their gradients, None where there are none."""
+    if x.dim() != 2 or y.shape != x.shape:
+        raise ValueError("norm: x %s, y %s" % (tuple(x.shape), tuple(y.shape)))
+    rows, H = x.shape
+    params = [t for t in params if t is not None]
+    for t in params:
+        _need(t, params[0].dtype, (H,), "weight, bias and their gradients")
+    pdt = _dt(params[0]) if params else DT["f32"]
+    return MoeNormDesc(rows, H, int(rms), _same_dt(x, y), pdt, eps, _step(x, 0), _step(y, 0))
+
+
+def moe_norm(x, weight, bias, y, eps=1e-5, rms=False, stats=None, stream=None):
+    """y = layer norm of the rows of x [rows, H] (RMS norm with rms=True), times `weight` [H] and plus `bias` [H] (None: without);
+    `stats`: optional float32 [rows, 2] that takes every row's mean and 1 / sqrt(variance + eps) for the backward pass."""
+    d = _norm_desc(x, y, (weight, bias), eps, rms)
+    if stats is not None:
+        _need(stats, torch.float32, (d.rows, 2), "stats")
+    _launch(lib().moe_norm, (ctypes.byref(d), _rowp(x), _ptr(weight), _ptr(bias), _rowp(y), _ptr(stats)),
+            (x, weight, bias, y, stats), stream)
+
+
+def moe_norm_workspace(rows, H) -> int:
+    return int(lib().moe_norm_workspace(rows, H))
+
+
+def moe_norm_grad(dy, x, weight, stats, dx, dweight=None, dbias=None, add=None, rms=False, ws=None, stream=None):
+    """Gradients of moe_norm: dx [rows, H] (plus `add`, a gradient that reaches x on another way), dweight and dbias [H] where
+    given.  `ws`: device workspace of at least moe_norm_workspace bytes (allocated here if None)."""
+    d = _norm_desc(x, dy, (weight, dweight, dbias), 0.0, rms)
+    _need(stats, torch.float32, (d.rows, 2), "stats")
+    _need(dx, x.dtype, x.shape, "dx")
+    if add is not None:
+        _need(add, x.dtype, x.shape, "add")
+    ws, wp, wn = _own_ws(ws, lambda: moe_norm_workspace(d.rows, d.H), x.device, stream)
+    _launch(lib().moe_norm_grad,
+            (ctypes.byref(d), _rowp(dy), _rowp(x), _ptr(weight), _ptr(stats), _ptr(add), _ptr(dx), _ptr(dweight), _ptr(dbias),
+             wp, wn), (x, dy, weight, stats, add, dx, dweight, dbias, ws), stream)
+
+
+def _own_ws(ws, need, device, stream):
+    """The workspace of a call, allocated here if None: tensor, address, bytes."""
+    _check_stream(stream, device.index)
+    if ws is None:
+        n = need()
+        if n:
+            ws = torch.empty(n, dtype=torch.uint8, device=device)
+            if stream is not None:  # used there, allocated (and freed on return) on the current stream
+                stream.wait_stream(torch.cuda.current_stream(device))
+                ws.record_stream(stream)
+    return ws, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _is_dense(t):
+    """Whether the elements of t fill one block of memory, in whatever order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for step, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if step != want:
+            return False
+        want *= n
+    return True
+
+
+def _tensor_list(grads, outs):
+    """moe_tensor entries of a list of gradients and of where their results go (an array of four 64-bit words each)."""
+    words = array.array("q")
+    for i, g in enumerate(grads):
+        if not g.is_cuda or not _is_dense(g):
+            raise ValueError("gradient %d: a device tensor without gaps expected" % i)
+        o = None if outs is None else outs[i]
+        if o is not None and (o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() or not o.is_cuda):
+            raise ValueError("result %d does not have its gradient's type, shape and strides" % i)
+        words.extend((g.data_ptr(), 0 if o is None else o.data_ptr(), g.numel(), _dt(g)))
+    return words
+
+
+def _grad_norm(f, grads, outs, args, norm, ws, stream):
+    _need(norm, torch.float32, (1,), "norm")
+    words = _tensor_list(grads, outs)
+    at, n = words.buffer_info()[0], len(grads)
+    ws, wp, wn = _own_ws(ws, lambda: int(lib().moe_grad_norm_workspace(at, n)), norm.device, stream)
+    _launch(f, (at, n, *args, _ptr(norm), wp, wn), (norm, ws, *grads, *(outs or ())), stream)
+
+
+def moe_grad_norm_workspace(grads) -> int:
+    words = _tensor_list(grads, None)
+    return int(lib().moe_grad_norm_workspace(words.buffer_info()[0], len(grads)))
+
+
+def moe_grad_norm(grads, norm, ws=None, stream=None):
+    """norm (float32 [1]) = the 2-norm over all elements of the tensors of the list `grads` (bfloat16 and float32).  `ws`: device
+    workspace of at least moe_grad_norm_workspace bytes (allocated here if None)."""
+    _grad_norm(lib().moe_grad_norm, grads, None, (), norm, ws, stream)
+
+
+def moe_clip_grad_norm(grads, max_norm, norm, outs=None, ws=None, stream=None):
+    """moe_grad_norm, then every gradient times min(1, max_norm / norm): in place, or into the tensors of `outs` (same types,
+    shapes and strides; None among them: not written).  A norm that is not finite scales nothing."""
+    if outs is None:
+        outs = grads
+    elif len(outs) != len(grads):
+        raise ValueError("%d gradients, %d results" % (len(grads), len(outs)))
+    _grad_norm(lib().moe_clip_grad_norm, grads, outs, (float(max_norm),), norm, ws, stream)
 
 
 def moe_combine(y_perm, topk_w, inv_perm, k, shared_y, out, stream=None):

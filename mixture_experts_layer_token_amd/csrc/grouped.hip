@@ -75,7 +75,7 @@ bool few_rows_kernel(int type, bool staged, int rows, int N, int E) {
 // 32 experts of 5760 x 2880 594 : 681, 4096 rows 264 : 302, 2036 rows over 128 experts of 2880 x 2880 473 : 393; weight gradient of 8192 rows, 4096 x
 // 4096, 197 : 250.  Small against deep: 1024 rows x 4096 x 4096 48 : 38.
 TileShape cheapest_shape(const GroupArgs& a, int op, int eb, double large, double small, double rows) {
-  const double c = op == kOpY ? a.K : op == kOpDx ? a.N : (double)a.rows / a.E;
+  const double c = op == kOpY || op == kOpGlu ? a.K : op == kOpDx || op == kOpGluDx ? a.N : (double)a.rows / a.E;
   const double ns = std::max(1.0, std::ceil(c * eb / 128));
   const double fl = std::max(0.6, rows / 256), fs = std::max(0.6, std::min(1.0, rows / 128));
   const double cus = cu_count();
@@ -100,14 +100,13 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   // direct loads: operand rows on 16-byte boundaries
   const int eb = type == kI8 ? 1 : type == kBf16 ? 2 : 4;
   auto al = [&](const void* p, long long ld) { return (uintptr_t)p % 16 == 0 && ld * eb % 16 == 0; };
-  const bool ax = op == kOpDx || (al(a.x, a.ldx) && a.K * eb % 16 == 0);
+  const bool forward = op == kOpY || op == kOpGlu, to_rows = op == kOpDx || op == kOpGluDx;
+  const bool ax = to_rows || (al(a.x, a.ldx) && a.K * eb % 16 == 0);
   const bool aw = op == kOpDw || (al(a.w, a.ldw) && a.w_stride * eb % 16 == 0 && a.K * eb % 16 == 0);
-  const bool ay = op == kOpY || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
+  const bool ay = forward || (al(a.y, a.ldy) && a.N * eb % 16 == 0);
   TileShape t = ax && aw && ay && tile_spans_fit(a, op, eb) ? kLarge : kStaged;
-  if (op == kOpY) {
-    if (few_rows_kernel(type, t == kStaged, a.rows, a.N, a.E))
-      return launch_grouped_decode(a, type, t == kLarge, s);
-  }
+  if (forward && few_rows_kernel(type, t == kStaged, a.rows, op == kOpGlu ? 2 * a.N : a.N, a.E))
+    return op == kOpGlu ? launch_glu_decode(a, type, t == kLarge, s) : launch_grouped_decode(a, type, t == kLarge, s);
   if (op == kOpDw) {
     const int split = dw_split(type, t == kStaged, a.rows, a.N, a.K, a.E);
     if (split > 1) {
@@ -126,7 +125,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   }
   // tiles of b x b (row counts are known on average only: half a tile more per group)
   const double avg = (double)a.rows / a.E;
-  const long long nj = op == kOpY ? a.N : a.K;
+  const long long nj = op == kOpGlu ? 2LL * a.N : forward ? a.N : a.K;
   auto tiles = [&](int b) {
     const double ni = op == kOpDw ? (double)((a.N + b - 1) / b) : a.E == 1 ? (double)((a.rows + b - 1) / b) : std::max(1.0, avg / b + 0.5);
     return ni * a.E * ((nj + b - 1) / b);
@@ -138,6 +137,10 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
   // experts with 540 to 1000 rows 1228 -> 906 us); small ones stay on one XCD, whose L2 then holds their rows (16384 rows over 16
   // experts of 1024 x 1024: 50 against 61 us).
   a.each_xcd = tiles(t == kLarge ? 256 : 128) >= 128.0 * a.E;
+  if (op == kOpGlu || op == kOpGluDx) {
+    if (type == kF32) return launch_tile_glu_f32(a, op, t, s);
+    return op == kOpGlu ? launch_tile_glu_bf16(a, t, s) : launch_tile_gludx_bf16(a, t, s);
+  }
   if (type == kF32) return launch_tile_f32(a, op, t, s);
   if (type == kI8) return launch_tile_y_i8(a, t, s);
   return op == kOpY ? launch_tile_y_bf16(a, t, s) : op == kOpDx ? launch_tile_dx_bf16(a, t, s) : launch_tile_dw_bf16(a, t, s);

@@ -5,7 +5,9 @@
 
 namespace moe {
 
-enum GroupOp { kOpY = 0, kOpDx = 1, kOpDw = 2 };
+// kOpGlu: the gated block, y = SiLU(x wg^T) (x wu^T) with w = [wg; wu] of 2N rows; kOpGluDx: the gradient of rows, on to
+// the gate's operands
+enum GroupOp { kOpY = 0, kOpDx = 1, kOpDw = 2, kOpGlu = 3, kOpGluDx = 4 };
 
 // One call.  x, w, y name the matrices of the forward product: for the gradient of the rows x is dx
 // (written) and y is dy, for that of the weights w is dw (written) and y is dy.
@@ -26,6 +28,11 @@ struct GroupArgs {
   // [split][E][N][K]
   int split;
   int each_xcd;  // tile kernel: every group's tiles are shared out over the XCDs (else a range of all tiles to each)
+  // gated block: rows [g | u], contiguous.  kOpGlu: written with y unless null; kOpGluDx: read, and dgu written, and h = SiLU(g) u
+  // again unless null (x is not: there is no dh in memory)
+  void* gu;
+  void* dgu;
+  void* h;
 };
 
 // Rows of expert e, clamped so that no offsets, however wrong, lead outside [0, rows).
@@ -120,8 +127,10 @@ constexpr long long kMaxSpan = 0xFFFF0000LL;  // bytes a buffer descriptor of th
 // Whether every descriptor of the kernel covers its operand: rows of a tile, or all of x where it is gathered, within
 // 32-bit offsets.
 inline bool tile_spans_fit(const GroupArgs& a, int op, int eb) {
+  if (op == kOpGluDx) op = kOpDx;
   auto rows = [&](long long n, long long ld) { return (n - 1) * ld * eb + ld * eb <= kMaxSpan && ld * eb < kMaxSpan / 512; };
   const bool x = a.perm_src ? a.x_rows == 0 || rows(a.x_rows, a.ldx) : rows(256, a.ldx);
+  if (op == kOpGlu) return x && rows((long long)a.N + 128, a.ldw);  // a tile's gate and up rows lie N rows apart
   return (op == kOpDx || x) && (op == kOpDw || rows(256, a.ldw)) && (op == kOpY || rows(256, a.ldy));
 }
 
@@ -135,9 +144,13 @@ int launch_tile_dx_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_dw_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_dw_bf16_gather(const GroupArgs& a, TileShape t, hipStream_t s);
 int launch_tile_f32(const GroupArgs& a, int op, TileShape t, hipStream_t s);
+int launch_tile_glu_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_gludx_bf16(const GroupArgs& a, TileShape t, hipStream_t s);
+int launch_tile_glu_f32(const GroupArgs& a, int op, TileShape t, hipStream_t s);
 constexpr int kDecodeRows = 64;  // rows of a workgroup there
 // grouped_decode.hip: forward for few rows; direct: rows on 16-byte boundaries and spans that fit
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s);
+int launch_glu_decode(const GroupArgs& a, int type, bool direct, hipStream_t s);
 // the kernel that suits the call; ws holds grouped_workspace bytes
 int launch_grouped(const GroupArgs& a, int op, int type, void* ws, hipStream_t s);
 size_t grouped_workspace(int type, int rows, int N, int K, int E);

@@ -1,4 +1,4 @@
-// C-ABI entry points of the grouped products over plain weights, of the 8-bit operators, of the SwiGLU gate
+// C-ABI entry points of the grouped products over plain weights, of the gated block, of the 8-bit operators, of the SwiGLU gate
 // and of the combine's gradient: argument validation, then the launches.
 #include "grouped.hpp"
 #include "rowwise.hpp"
@@ -9,8 +9,8 @@ namespace {
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 size_t dt_bytes(int dt) { return dt == MOE_BF16 ? 2 : 4; }
 
-// everything about the descriptor; bytes: of an x / w element
-int check_grouped(const moe_grouped* g, const char* fn) {
+// everything about the descriptor; w_rows: rows of w per output feature
+int check_grouped(const moe_grouped* g, const char* fn, int w_rows = 1) {
   if (!g) return fail(MOE_ERR_INVALID, "%s: null moe_grouped", fn);
   if (g->rows < 0 || g->rows > (1 << 24)) return fail(MOE_ERR_INVALID, "%s: rows=%d out of 0..1<<24", fn, g->rows);
   if (g->E < 1 || g->E > 1024) return fail(MOE_ERR_INVALID, "%s: E=%d out of 1..1024", fn, g->E);
@@ -24,7 +24,7 @@ int check_grouped(const moe_grouped* g, const char* fn) {
     return fail(MOE_ERR_INVALID, "%s: row strides %lld, %lld, %lld shorter than a row", fn, (long long)g->ldx,
                 (long long)g->ldw, (long long)g->ldy);
   const int64_t ldw = g->ldw ? g->ldw : g->K;
-  if (g->w_stride && (g->w_stride < (g->N - 1) * ldw + g->K || g->w_stride > kMaxLd))
+  if (g->w_stride && (g->w_stride < ((int64_t)w_rows * g->N - 1) * ldw + g->K || g->w_stride > kMaxLd))
     return fail(MOE_ERR_INVALID, "%s: expert stride %lld shorter than a matrix", fn, (long long)g->w_stride);
   if (!g->offsets || !aligned(g->offsets, 4) || !aligned(g->perm_src, 4))
     return fail(MOE_ERR_INVALID, "%s: null or misaligned offsets or perm_src", fn);
@@ -98,6 +98,46 @@ extern "C" int moe_grouped_gemm_dx(const moe_grouped* g, int dt, const void* dy,
 extern "C" int moe_grouped_gemm_dw(const moe_grouped* g, int dt, const void* dy, const void* x, void* dw, int dwdt,
                                    void* ws, size_t ws_bytes, void* stream) {
   return grouped_call("moe_grouped_gemm_dw", g, kOpDw, dt, x, dw, dy, dwdt, ws, ws_bytes, stream);
+}
+
+extern "C" int moe_grouped_swiglu(const moe_grouped* g, int dt, const void* x, const void* w, void* h, void* gu,
+                                  void* stream) {
+  const char* fn = "moe_grouped_swiglu";
+  if (!dtype_valid(dt)) return fail(MOE_ERR_INVALID, "%s: bad dtype %d", fn, dt);
+  int rc = check_grouped(g, fn, 2);
+  if (rc != MOE_OK) return rc;
+  const size_t b = dt_bytes(dt);
+  if (g->rows > 0 && (!w || !h || (!x && !(g->perm_src && g->x_rows == 0))))
+    return fail(MOE_ERR_INVALID, "%s: null pointer", fn);
+  if (!aligned(x, b) || !aligned(w, b) || !aligned(h, b) || !aligned(gu, b))
+    return fail(MOE_ERR_INVALID, "%s: pointer not aligned to its element type", fn);
+  if (g->rows == 0) return MOE_OK;
+  GroupArgs a = group_args(g, x, w, h, dt);
+  if (!g->w_stride) a.w_stride = 2 * a.ldw * g->N;
+  a.gu = gu;
+  return launch_grouped(a, kOpGlu, dt == MOE_BF16 ? kBf16 : kF32, nullptr, (hipStream_t)stream);
+}
+
+extern "C" int moe_grouped_swiglu_dx(const moe_grouped* g, int dt, const void* dy, const void* w, const void* gu,
+                                     void* dgu, void* h, void* stream) {
+  const char* fn = "moe_grouped_swiglu_dx";
+  if (!dtype_valid(dt)) return fail(MOE_ERR_INVALID, "%s: bad dtype %d", fn, dt);
+  moe_grouped d;
+  if (g) {  // (dgu has one row per grouped row, and rows of its own length)
+    d = *g;
+    d.perm_src = nullptr;
+    d.ldx = 0;
+  }
+  int rc = check_grouped(g ? &d : nullptr, fn);
+  if (rc != MOE_OK) return rc;
+  const size_t b = dt_bytes(dt);
+  if (d.rows > 0 && (!dy || !w || !gu || !dgu)) return fail(MOE_ERR_INVALID, "%s: null pointer", fn);
+  if (!aligned(dy, b) || !aligned(w, b) || !aligned(gu, b) || !aligned(dgu, b) || !aligned(h, b))
+    return fail(MOE_ERR_INVALID, "%s: pointer not aligned to its element type", fn);
+  if (d.rows == 0) return MOE_OK;
+  GroupArgs a = group_args(&d, nullptr, w, dy, dt);
+  a.gu = (void*)gu, a.dgu = dgu, a.h = h;
+  return launch_grouped(a, kOpGluDx, dt == MOE_BF16 ? kBf16 : kF32, nullptr, (hipStream_t)stream);
 }
 
 extern "C" int moe_grouped_gemm_i8(const moe_grouped* g, const int8_t* q, const float* q_scale, const int8_t* w,

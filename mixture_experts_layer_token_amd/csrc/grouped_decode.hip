@@ -55,17 +55,22 @@ struct Rows {
   }
 };
 
-template <int TYPE, bool DIRECT, int MT>
+// GLU: the gated block.  Gate and up rows of the same 16 features, so half as many bytes of weights per feature's worth of x;
+// the sums of the gate's strip pass through LDS first, then those of the up strip, and the same thread holds both.
+template <int TYPE, bool DIRECT, int MT, bool GLU>
 __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, int rows, int n0, char* smem) {
   typedef TileT<TYPE> TT;
   typedef typename TT::Frag Frag;
   typedef typename TT::Acc Acc;
-  constexpr int EB = TT::EB, D = MT == 1 ? 4 : MT == 2 ? 3 : 2;
+  constexpr int EB = TT::EB, D = MT == 1 ? 4 : MT == 2 ? 3 : 2, S = GLU ? 2 : 1;  // S: strips of 16 weight rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int len = a.K * EB, nj = min(kDecodeCols, a.N - n0);
-  Rows<EB, DIRECT> W, X[MT];
+  Rows<EB, DIRECT> W[S], X[MT];
   const gptr w = (gptr)a.w + ((size_t)e * a.w_stride + (size_t)n0 * a.ldw) * EB;
-  W.init(w, (unsigned)((nj - 1) * a.ldw * EB) + len, (long long)min(lane & 15, nj - 1) * a.ldw * EB, len);
+#pragma unroll
+  for (int z = 0; z < S; ++z)
+    W[z].init(w + (z ? (size_t)a.N * a.ldw * EB : 0), (unsigned)((nj - 1) * a.ldw * EB) + len,
+              (long long)min(lane & 15, nj - 1) * a.ldw * EB, len);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = p0 + min(16 * m + (lane & 15), rows - 1);
@@ -79,7 +84,7 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
   }
   // group g: bytes 128 g .. 128 g + 127 of every row, as two MFMA operands per lane
   struct Group {
-    u32x4 w[2], x[2][MT];
+    u32x4 w[2][S], x[2][MT];
   };
   const int c0 = (lane >> 4) * 16;
   auto load = [&](Group& G, int g) {
@@ -87,14 +92,17 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = g * 128 + h * 64 + c0;
-      G.w[h] = W.load(c, whole, len);
+#pragma unroll
+      for (int z = 0; z < S; ++z) G.w[h][z] = W[z].load(c, whole, len);
 #pragma unroll
       for (int m = 0; m < MT; ++m) G.x[h][m] = X[m].load(c, whole, len);
     }
   };
-  Acc acc[MT];
+  Acc acc[S][MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = Acc{};
+  for (int z = 0; z < S; ++z)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[z][m] = Acc{};
   const int ng = (len + 127) / 128;
   Group ring[D];
 #pragma unroll
@@ -106,15 +114,41 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[m] = mma(__builtin_bit_cast(Frag, ring[d].w[h]), __builtin_bit_cast(Frag, ring[d].x[h][m]), acc[m]);
+#pragma unroll
+          for (int z = 0; z < S; ++z)
+            acc[z][m] = mma(__builtin_bit_cast(Frag, ring[d].w[h][z]), __builtin_bit_cast(Frag, ring[d].x[h][m]), acc[z][m]);
       load(ring[d], g + (d + D) * nw);
     }
   }
   // the waves' sums, in wave order
   Acc* part = (Acc*)smem;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[m];
+  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[0][m];
   __syncthreads();
+  if constexpr (GLU) {
+    const int t = threadIdx.x, m = t >> 6, i = 16 * m + (t & 15), jj = ((t & 63) >> 4) * 4;
+    const bool mine = t < MT * 64 && i < rows;  // (MT * 64 <= blockDim.x)
+    Acc g = Acc{}, u = Acc{};
+    if (mine)
+      for (int o = 0; o < nw; ++o) g += part[o * MT * 64 + t];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < MT; ++q) part[(wave * MT + q) * 64 + lane] = acc[S - 1][q];
+    __syncthreads();
+    if (!mine) return;
+    for (int o = 0; o < nw; ++o) u += part[o * MT * 64 + t];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (jj + r >= nj) break;
+      const size_t p = (size_t)(p0 + i);
+      const int j = n0 + jj + r;
+      store_out((void*)a.y, p * a.ldy + j, g[r] / (1.f + expf(-g[r])) * u[r], EB == 2);
+      if (!a.gu) continue;
+      store_out(a.gu, p * 2 * a.N + j, g[r], EB == 2);
+      store_out(a.gu, p * 2 * a.N + a.N + j, u[r], EB == 2);
+    }
+    return;
+  }
   for (int t = threadIdx.x; t < MT * 64; t += blockDim.x) {
     const int m = t >> 6, i = 16 * m + (t & 15), jj = ((t & 63) >> 4) * 4;
     if (i >= rows) continue;
@@ -136,7 +170,7 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
   }
 }
 
-template <int TYPE, bool DIRECT>
+template <int TYPE, bool DIRECT, bool GLU>
 __global__ __launch_bounds__(512) void grouped_decode_kernel(GroupArgs a) {
   __shared__ __align__(16) char smem[8 * 4 * 64 * 16];
   const int ncol = (a.N + kDecodeCols - 1) / kDecodeCols;
@@ -147,11 +181,11 @@ __global__ __launch_bounds__(512) void grouped_decode_kernel(GroupArgs a) {
   const int r0 = tile * kDecodeRows, rows = min(kDecodeRows, g.n - r0), mt = (rows + 15) / 16;
   static_for<kDecodeRows / 16>([&](auto mc) {
     constexpr int MT = mc + 1;
-    if (mt == MT) decode_body<TYPE, DIRECT, MT>(a, g.e, g.p0 + r0, rows, col * kDecodeCols, smem);
+    if (mt == MT) decode_body<TYPE, DIRECT, MT, GLU>(a, g.e, g.p0 + r0, rows, col * kDecodeCols, smem);
   });
 }
 
-template <int TYPE>
+template <int TYPE, bool GLU = false>
 int decode_launch(const GroupArgs& a, bool direct, hipStream_t s) {
   const long long nb = group_tiles_max(a.rows, a.E, kDecodeRows) * ((a.N + kDecodeCols - 1) / kDecodeCols);
   if (nb == 0) return MOE_OK;
@@ -159,9 +193,9 @@ int decode_launch(const GroupArgs& a, bool direct, hipStream_t s) {
   const int threads = nb < 1024 ? 512 : 256;
   if (nb > kMaxThreads / threads) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
   if (direct)
-    hipLaunchKernelGGL((grouped_decode_kernel<TYPE, true>), dim3((unsigned)nb), dim3(threads), 0, s, a);
+    hipLaunchKernelGGL((grouped_decode_kernel<TYPE, true, GLU>), dim3((unsigned)nb), dim3(threads), 0, s, a);
   else
-    hipLaunchKernelGGL((grouped_decode_kernel<TYPE, false>), dim3((unsigned)nb), dim3(threads), 0, s, a);
+    hipLaunchKernelGGL((grouped_decode_kernel<TYPE, false, GLU>), dim3((unsigned)nb), dim3(threads), 0, s, a);
   MOE_CHECK_LAUNCH("moe_grouped_gemm launch");
   return MOE_OK;
 }
@@ -171,6 +205,9 @@ int decode_launch(const GroupArgs& a, bool direct, hipStream_t s) {
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s) {
   return type == kI8 ? decode_launch<kI8>(a, direct, s)
                      : type == kF32 ? decode_launch<kF32>(a, direct, s) : decode_launch<kBf16>(a, direct, s);
+}
+int launch_glu_decode(const GroupArgs& a, int type, bool direct, hipStream_t s) {
+  return type == kF32 ? decode_launch<kF32, true>(a, direct, s) : decode_launch<kBf16, true>(a, direct, s);
 }
 
 }  // namespace moe

@@ -331,14 +331,20 @@ struct TileKernel {
   typedef typename TT::Acc Acc;
   static constexpr int EB = TT::EB, KE = kStageC / EB;  // elements of c per stage
   static constexpr int BI = 32 * WI, BJ = 32 * WJ;
-  static constexpr bool SA = OP == kOpDw, SB = OP != kOpY;  // strided operands
+  // the product behind the operator, and whether the gate follows it in the same tile
+  static constexpr bool GLU = OP == kOpGlu, GDX = OP == kOpGluDx;
+  static constexpr int DIR = GLU ? kOpY : GDX ? kOpDx : OP;
+  // GLU: the tile's rows of B are strips of 16 rows of the gate's matrix and of the up matrix in turn, so that a lane's
+  // accumulators of strips 2s and 2s + 1 hold g and u of the same row and columns
+  static constexpr int COLS = GLU ? BJ / 2 : BJ;  // columns of the result
+  static constexpr bool SA = DIR == kOpDw, SB = DIR != kOpY;  // strided operands
   typedef typename std::conditional<SA, Strided<BI, EB>, Contig<BI, EB>>::type OpA;
   typedef typename std::conditional<SB, Strided<BJ, EB>, Contig<BJ, EB>>::type OpB;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
   static constexpr int NL = OpA::LQ + OpB::LQ;           // loads per stage and wave
   static constexpr int REGION = 16 * 16 * WJ * 4;        // per wave, behind the stages: see store_rows
   static constexpr size_t LDS = (size_t)NB * STAGE + kWaves * REGION;
-  static constexpr bool IDX = GATHER && OP == kOpDw && !STAGED;  // x rows of c through perm_src
+  static constexpr bool IDX = GATHER && DIR == kOpDw && !STAGED;  // x rows of c through perm_src
   static constexpr int RPL = IDX ? 1024 / (BJ * EB) : 1;  // c rows per load of B
   static constexpr int NX = IDX ? OpB::LQ * RPL : 1;
   static_assert(NB == 2 || (NB == 4 && !STAGED), "stages");
@@ -356,7 +362,7 @@ struct TileKernel {
     int idx_next[NX];
     unsigned idx[NX], bcol[OpB::LQ];
     // offsets of the gathered x rows of the tile to come
-    static constexpr bool AHEAD = OP == kOpY && !STAGED;
+    static constexpr bool AHEAD = DIR == kOpY && !STAGED;
     unsigned ahead[AHEAD ? OpA::LQ : 1];
     // STAGED: a stage in registers
     u32x4 held[STAGED ? NL : 1];
@@ -376,26 +382,31 @@ struct TileKernel {
         }
       }
     }
+    // row of w behind row r of B, from row j0 (DIR == kOpY)
+    __device__ __forceinline__ int b_row(int r) const {
+      if constexpr (GLU) return min(r / 32 * 16 + r % 16, t.nj - 1) + (r / 16 % 2 ? a.N : 0);
+      return min(r, t.nj - 1);
+    }
     __device__ __forceinline__ void init(const TileItem& item) {
       t = item;
       const gptr x = (gptr)a.x, w = (gptr)a.w + (size_t)t.e * a.w_stride * EB, y = (gptr)a.y;
       const unsigned ldx = (unsigned)a.ldx * EB, ldw = (unsigned)a.ldw * EB, ldy = (unsigned)a.ldy * EB;
       if constexpr (STAGED) {
         fetched = 0;
-        if constexpr (OP == kOpY) {
+        if constexpr (DIR == kOpY) {
           A.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr {
             const int xr = x_row(a, t.p0 + min(r, t.ni - 1));
             return xr >= 0 ? x + (size_t)xr * a.ldx * EB : (gptr) nullptr;
           });
-          B.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr { return w + (size_t)(t.j0 + min(r, t.nj - 1)) * a.ldw * EB; });
-        } else if constexpr (OP == kOpDx) {
+          B.init_fetch(wave, lane, a.K * EB, [&](int r) -> gptr { return w + (size_t)(t.j0 + b_row(r)) * a.ldw * EB; });
+        } else if constexpr (DIR == kOpDx) {
           A.init_fetch(wave, lane, a.N * EB, [&](int r) -> gptr { return y + (size_t)(t.p0 + min(r, t.ni - 1)) * a.ldy * EB; });
           B.init_fetch(w + (size_t)t.j0 * EB, a.ldw * EB, t.nc, t.nj * EB);
         } else {
           A.init_fetch(y + ((size_t)t.p0 * a.ldy + t.i0) * EB, a.ldy * EB, t.nc, t.ni * EB);
           B.init_fetch(x + ((size_t)(GATHER ? 0 : t.p0) * a.ldx + t.j0) * EB, a.ldx * EB, t.nc, t.nj * EB);
         }
-      } else if constexpr (OP == kOpY) {
+      } else if constexpr (DIR == kOpY) {
         const unsigned cb = (unsigned)a.K * EB;
         if (a.perm_src)
           A.init(wave, lane, x, a.x_rows > 0 ? (unsigned)(a.x_rows - 1) * ldx + cb : 0, cb,
@@ -403,9 +414,9 @@ struct TileKernel {
         else
           A.init(wave, lane, x + (size_t)t.p0 * a.ldx * EB, (unsigned)(t.ni - 1) * ldx + cb, cb,
                  [&](int r, int) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldx; });
-        B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1) * ldw + cb, cb,
-               [&](int r, int) -> unsigned { return (unsigned)min(r, t.nj - 1) * ldw; });
-      } else if constexpr (OP == kOpDx) {
+        B.init(wave, lane, w + (size_t)t.j0 * a.ldw * EB, (unsigned)(t.nj - 1 + (GLU ? a.N : 0)) * ldw + cb, cb,
+               [&](int r, int) -> unsigned { return (unsigned)b_row(r) * ldw; });
+      } else if constexpr (DIR == kOpDx) {
         const unsigned cb = (unsigned)a.N * EB;
         A.init(wave, lane, y + (size_t)t.p0 * a.ldy * EB, (unsigned)(t.ni - 1) * ldy + cb, cb,
                [&](int r, int) -> unsigned { return (unsigned)min(r, t.ni - 1) * ldy; });
@@ -475,7 +486,7 @@ struct TileKernel {
 
     // a stage into registers
     __device__ __forceinline__ void fetch() {
-      const bool tiny_a = (OP == kOpY ? a.K : a.N) * EB < 16, tiny_b = a.K * EB < 16;  // bytes of the operands' rows
+      const bool tiny_a = (DIR == kOpY ? a.K : a.N) * EB < 16, tiny_b = a.K * EB < 16;  // bytes of the operands' rows
       if (tiny_a || tiny_b) fetch_stage<true>();
       else fetch_stage<false>();
       A.end_fetch();
@@ -484,7 +495,7 @@ struct TileKernel {
     }
     template <bool TINY>
     __device__ __forceinline__ void fetch_stage() {
-      constexpr bool GB = GATHER && OP == kOpDw;
+      constexpr bool GB = GATHER && DIR == kOpDw;
       int xr[GB ? OpB::LQ : 1];
 #pragma unroll
       for (int q = 0; q < OpA::LQ; ++q) {
@@ -538,6 +549,171 @@ struct TileKernel {
       }
     }
   };
+
+  // The gate behind the sums.  bf16: the hardware's exponential and reciprocal, off by about 2^-17 of the value where the
+  // result is rounded by up to 2^-9 (the accurate ones take 6 us per tile of 256 x 256 instead of 3); fp32: the accurate ones.
+  static __device__ __forceinline__ float sigmoid(float g) {
+    if constexpr (TYPE == kBf16) return __builtin_amdgcn_rcpf(1.f + __expf(-g));
+    return 1.f / (1.f + expf(-g));
+  }
+  // 4 neighbouring elements of a row of the operands' type
+  static __device__ __forceinline__ void store4(char* p, const float (&v)[4]) {
+    if constexpr (TYPE == kBf16) *(u32x2*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    else *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+  }
+
+  // Results of the gated block: h = SiLU(g) u from the unrounded sums, and [g | u] itself if it is kept.
+  template <int NI>
+  static __device__ __forceinline__ void write_glu(const GroupArgs& a, const TileItem& t, const Feed& feed, Acc (&acc)[WJ][NI]) {
+    const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
+    const int rlane = wi * 16 + (lane & 15), clane = WJ / 2 * wj * 16 + (lane >> 4) * 4;  // as in body()
+    const bool keep = a.gu != nullptr;
+    const long long ldg = 2LL * a.N;
+    char* h = (char*)a.y + ((size_t)t.p0 * a.ldy + t.j0) * EB;
+    char* gu = (char*)a.gu + ((size_t)t.p0 * ldg + t.j0) * EB;
+    if constexpr (!STAGED) wait_loads<0>();
+    if (((size_t)h | (size_t)(a.ldy * EB)) % (4 * EB) == 0 && (size_t)a.gu % (4 * EB) == 0 && a.N % 4 == 0) {
+      auto rows = [&](auto kept) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int r = 32 * i + rlane;
+          if (r >= t.ni) continue;
+          char* p = h + ((size_t)r * a.ldy + clane) * EB;
+          char* q = gu + ((size_t)r * ldg + clane) * EB;
+#pragma unroll
+          for (int j = 0; j < WJ / 2; ++j) {
+            if (clane + 16 * j >= t.nj) continue;
+            float g[4], u[4], v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              g[e] = acc_get(acc[2 * j][i], e), u[e] = acc_get(acc[2 * j + 1][i], e);
+              v[e] = g[e] * sigmoid(g[e]) * u[e];
+            }
+            store4(p + 16 * j * EB, v);
+            if constexpr (decltype(kept)::value) {
+              store4(q + 16 * j * EB, g);
+              store4(q + ((size_t)a.N + 16 * j) * EB, u);
+            }
+          }
+        }
+      };
+      if (keep) rows(std::true_type{});
+      else rows(std::false_type{});
+    } else {
+      // any other: 16 rows at a time through the wave's own LDS region (g, then u behind it), element by element
+      typedef __attribute__((address_space(3))) float* lfloat;
+      constexpr int W = 16 * WJ / 2;
+      const lfloat reg = (lfloat)(feed.lds + NB * STAGE + wave * REGION);
+      const int c0 = WJ / 2 * wj * 16, nj = min(t.nj - c0, W);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc_get(acc[j][i], e);
+          *(__attribute__((address_space(3))) f32x4*)(reg + (j & 1) * 16 * W + (lane & 15) * W + j / 2 * 16 + (lane >> 4) * 4) = v;
+        }
+        const int r0 = 32 * i + wi * 16;
+#pragma unroll 1
+        for (int r = 0; r < min(t.ni - r0, 16); ++r)
+#pragma unroll 1
+          for (int c = lane; c < nj; c += 64) {
+            const float g = reg[r * W + c], u = reg[(16 + r) * W + c];
+            store_out(h, (size_t)(r0 + r) * a.ldy + c0 + c, g * sigmoid(g) * u, EB == 2);
+            if (!keep) continue;
+            store_out(gu, (size_t)(r0 + r) * ldg + c0 + c, g, EB == 2);
+            store_out(gu, (size_t)(r0 + r) * ldg + a.N + c0 + c, u, EB == 2);
+          }
+      }
+    }
+  }
+
+  // Results of the block's gradient: with dh the sums, s = 1 / (1 + e^-g),
+  //   dgu = [dh u s (1 + g (1 - s)) | dh g s],  h = g s u
+  template <int NI>
+  static __device__ __forceinline__ void write_glu_dx(const GroupArgs& a, const TileItem& t, const Feed& feed, Acc (&acc)[WJ][NI]) {
+    const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
+    const int rlane = wi * 16 + (lane & 15), clane = WJ * wj * 16 + (lane >> 4) * 4;
+    const long long ldg = 2LL * a.K;
+    const size_t o = ((size_t)t.p0 * ldg + t.j0) * EB;
+    const char* gu = (const char*)a.gu + o;
+    char* dgu = (char*)a.dgu + o;
+    char* h = (char*)a.h + ((size_t)t.p0 * a.K + t.j0) * EB;
+    auto grad = [](float dh, float g, float u, float& dg, float& du, float& hv) {
+      const float s = sigmoid(g);
+      dg = dh * u * s * (1.f + g * (1.f - s));
+      du = dh * g * s;
+      hv = g * s * u;
+    };
+    if constexpr (!STAGED) wait_loads<0>();
+    if (((size_t)a.gu | (size_t)a.dgu | (size_t)a.h) % (4 * EB) == 0 && a.K % 4 == 0) {
+      auto rows = [&](auto with_h) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int r = 32 * i + rlane;
+          if (r >= t.ni) continue;
+          const size_t q = ((size_t)r * ldg + clane) * EB;
+#pragma unroll
+          for (int j = 0; j < WJ; ++j) {
+            if (clane + 16 * j >= t.nj) continue;
+            float g[4], u[4], dg[4], du[4], hv[4];
+            load4(gu + q + 16 * j * EB, g);
+            load4(gu + q + ((size_t)a.K + 16 * j) * EB, u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) grad(acc_get(acc[j][i], e), g[e], u[e], dg[e], du[e], hv[e]);
+            store4(dgu + q + 16 * j * EB, dg);
+            store4(dgu + q + ((size_t)a.K + 16 * j) * EB, du);
+            if constexpr (decltype(with_h)::value) store4(h + ((size_t)r * a.K + clane + 16 * j) * EB, hv);
+          }
+        }
+      };
+      if (a.h) rows(std::true_type{});
+      else rows(std::false_type{});
+    } else {
+      typedef __attribute__((address_space(3))) float* lfloat;
+      constexpr int W = 16 * WJ;
+      const lfloat reg = (lfloat)(feed.lds + NB * STAGE + wave * REGION);
+      const int c0 = WJ * wj * 16, nj = min(t.nj - c0, W);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc_get(acc[j][i], e);
+          *(__attribute__((address_space(3))) f32x4*)(reg + (lane & 15) * W + 16 * j + (lane >> 4) * 4) = v;
+        }
+        const int r0 = 32 * i + wi * 16;
+#pragma unroll 1
+        for (int r = 0; r < min(t.ni - r0, 16); ++r)
+#pragma unroll 1
+          for (int c = lane; c < nj; c += 64) {
+            const size_t q = (size_t)(r0 + r) * ldg + c0 + c;
+            float dg, du, hv;
+            grad(reg[r * W + c], load1(gu, q), load1(gu, q + a.K), dg, du, hv);
+            store_out(dgu, q, dg, EB == 2);
+            store_out(dgu, q + a.K, du, EB == 2);
+            if (a.h) store_out(h, (size_t)(r0 + r) * a.K + c0 + c, hv, EB == 2);
+          }
+      }
+    }
+  }
+  static __device__ __forceinline__ void load4(const char* p, float (&v)[4]) {
+    if constexpr (TYPE == kBf16) {
+      const u32x2 b = *(const u32x2*)p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(e % 2 ? b[e / 2] & 0xFFFF0000u : b[e / 2] << 16);
+    } else {
+      const f32x4 b = *(const f32x4*)p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = b[e];
+    }
+  }
+  static __device__ __forceinline__ float load1(const char* p, size_t i) {
+    if constexpr (TYPE == kBf16) return bf16_to_f32(((const unsigned short*)p)[i]);
+    return ((const float*)p)[i];
+  }
 
   // One tile with NI row fragments per wave.  Its first NB stages have landed for this wave (STAGED: feed is
   // initialised).  advance() is called when the tile's last operands have been read: it starts the loads of the
@@ -631,6 +807,8 @@ struct TileKernel {
     barrier_keep_loads();
     advance();
 
+    if constexpr (GLU) return write_glu<NI>(a, t, feed, acc);
+    if constexpr (GDX) return write_glu_dx<NI>(a, t, feed, acc);
     // ---- results
     // A lane's four results are neighbouring columns of one row: 8 or 16 bytes per store, straight from the
     // accumulators.  The code is kept short on purpose: with every address and rounding spelled out it took 28 us
@@ -719,7 +897,7 @@ template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB>
 __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped_tile_kernel(GroupArgs a) {
   typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
   extern __shared__ __align__(1024) char smem[];
-  const int nj = OP == kOpY ? a.N : a.K, ncol = (nj + Tk::BJ - 1) / Tk::BJ;
+  const int nj = Tk::DIR == kOpY ? a.N : a.K, ncol = (nj + Tk::COLS - 1) / Tk::COLS;
   const int ntw = (a.N + Tk::BI - 1) / Tk::BI;  // row tiles of a weight gradient
   const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
   // This XCD's tiles: its part of every group, or (few tiles per group) a contiguous range of all of them
@@ -779,10 +957,10 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
         band_order(g.tile, nt, ncol, row, col);
         const int each = g.n / nt, longer = g.n - each * nt;  // the first `longer` tiles have one row more
         t.p0 = g.p0 + row * each + min(row, longer), t.ni = each + (row < longer), t.i0 = 0;
-        t.nc = OP == kOpY ? a.K : a.N;
+        t.nc = Tk::DIR == kOpY ? a.K : a.N;
       }
-      t.j0 = col * Tk::BJ;
-      t.nj = min(Tk::BJ, nj - t.j0);
+      t.j0 = col * Tk::COLS;
+      t.nj = min(Tk::COLS, nj - t.j0);
       // everything about the tile is uniform
       t.i0 = uni(t.i0), t.ni = uni(t.ni), t.j0 = uni(t.j0), t.nj = uni(t.nj), t.p0 = uni(t.p0), t.nc = uni(t.nc);
       if (OP != kOpDw || t.nc > 0) {
@@ -829,10 +1007,10 @@ __global__ __launch_bounds__(256, (WI * WJ > 16 || NB > 2 ? 1 : 2)) void grouped
 template <int OP, int TYPE, int WI, int WJ, bool GATHER, bool STAGED, int NB = 2>
 int tile_launch_one(const GroupArgs& a, hipStream_t s) {
   typedef TileKernel<OP, TYPE, WI, WJ, GATHER, STAGED, NB> Tk;
-  const int nj = OP == kOpY ? a.N : a.K;
+  const int nj = Tk::DIR == kOpY ? a.N : a.K;
   const long long nt = OP == kOpDw ? (long long)a.E * ((a.N + Tk::BI - 1) / Tk::BI) * a.split
                                    : group_tiles_max(a.rows, a.E, Tk::BI);
-  long long nb = nt * ((nj + Tk::BJ - 1) / Tk::BJ);
+  long long nb = nt * ((nj + Tk::COLS - 1) / Tk::COLS);
   if (nb == 0) return MOE_OK;
   if (nb > 0x7FFFFF00LL) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles", nb);
   static bool attr_set[64];  // per device

@@ -1,0 +1,508 @@
+// Layer norm and RMS norm of rows, and their gradients.  Bound by memory: every row is read once, held in registers through
+// its sums, and written once.
+//
+//   mean = sum x / H (RMS: 0),  rstd = 1 / sqrt(sum (x - mean)^2 / H + eps),  xh = (x - mean) rstd,  y = xh w + b
+//   dx = rstd (v - m1 - xh m2) (+ add),  v = w dy,  m1 = sum v / H (RMS: 0),  m2 = sum v xh / H
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// The variance is taken from the deviations (a second pass over registers), not from a difference of squares.  The sums over
+// rows stay in registers while a workgroup walks over its rows, one partial sum per workgroup goes to memory, and a second
+// kernel adds those up in order: no atomics, results are bitwise reproducible.
+#include <algorithm>
+#include <type_traits>
+
+#include "ffn_common.hpp"
+#include "norm.hpp"
+#include "operand.hpp"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------ 8 elements of a row
+
+// as they are in memory
+template <bool BF16>
+struct Raw {
+  u32x4 v[BF16 ? 1 : 2];
+};
+
+// Elements j .. j+7 of a row of n, zeros past its end, at any element-aligned address.  Without conditions, behind which
+// the loads of a row would wait for one another: a chunk that ends past the row reads the row's last 8 elements, and unpack()
+// moves them down.  Rows of less than 8 are read one by one.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void* row, int j, int n) {
+  constexpr int EB = BF16 ? 2 : 4;
+  Raw<BF16> r;
+  if (n < 8) {  // (uniform)
+    if constexpr (BF16) {
+      r.v[0] = load_part<2>((gptr)row + (size_t)j * 2, (n - j) * 2);
+    } else {
+      r.v[0] = load_part<4>((gptr)row + (size_t)j * 4, (n - j) * 4);
+      r.v[1] = load_part<4>((gptr)row + (size_t)j * 4 + 16, (n - j - 4) * 4);
+    }
+    return r;
+  }
+  const gptr p = (gptr)row + (size_t)min(j, n - 8) * EB;
+  r.v[0] = load_any(p);
+  if constexpr (!BF16) r.v[1] = load_any(p + 16);
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Raw<BF16>& r, int j, int n, float (&v)[8]) {
+  const int s = n < 8 ? 0 : max(j - (n - 8), 0);  // elements to move down; 8 and more: zeros
+  if constexpr (BF16) {
+    u32x4 b = r.v[0];
+    if (n % 8) b = shift_bytes(b, min(s, 8) * 2);
+    else if (s) b = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(b[i] << 16), v[2 * i + 1] = __uint_as_float(b[i] & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.v[i / 4][i % 4]);
+    if (n % 8) {
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) {
+        if (!(s & d)) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i + d < 8 ? v[(i + d) % 8] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = s >= 8 ? 0.f : v[i];
+  }
+}
+
+// two fp32 to bf16, nearest-even (one instruction)
+__device__ __forceinline__ unsigned pair_bf16(float lo, float hi) {
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 b2;
+  return __builtin_bit_cast(unsigned, b2{(__bf16)lo, (__bf16)hi});
+}
+template <bool BF16>
+__device__ __forceinline__ void store_chunk(void* row, int j, int n, const float (&v)[8]) {
+  typedef u32x4 __attribute__((aligned(1))) any4;
+  typedef __attribute__((address_space(1))) any4* anyp;
+  if (j + 8 <= n) {
+    if constexpr (BF16) {
+      *(anyp)((__attribute__((address_space(1))) char*)row + (size_t)j * 2) =
+          u32x4{pair_bf16(v[0], v[1]), pair_bf16(v[2], v[3]), pair_bf16(v[4], v[5]), pair_bf16(v[6], v[7])};
+    } else {
+      const anyp p = (anyp)((__attribute__((address_space(1))) char*)row + (size_t)j * 4);
+      p[0] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+      p[1] = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < n) {
+        if constexpr (BF16) ((unsigned short*)row)[j + i] = f32_to_bf16_rne(v[i]);
+        else ((float*)row)[j + i] = v[i];
+      }
+  }
+}
+
+// elements j .. j+7 of weight or bias (null: `none`), zeros past the end
+__device__ __forceinline__ void load_param(const void* p, int bf16, int j, int n, float none, float (&v)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = j + i < n ? none : 0.f;
+  } else if (bf16) {
+    unpack<true>(load_raw<true>(p, j, n), j, n, v);
+  } else {
+    unpack<false>(load_raw<false>(p, j, n), j, n, v);
+  }
+}
+
+// ------------------------------------------------------------------ sums over a row
+
+// over the wave, in a fixed order; every lane gets it.  (Row shifts and broadcasts cost an instruction each; the butterfly of
+// lane permutes goes through LDS.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xF>(v);  // lanes 1, 2, 4 and 8 below, in rows of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // the last lane of a row to the next row (rows 1 and 3)
+  v = dpp_add<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+// over the WPR waves of a row; part: WPR floats that no other sum uses until two barriers later
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  v = wave_sum(v);
+  if constexpr (WPR == 1) return v;
+  const int wave = threadIdx.x / 64 % WPR;
+  if ((threadIdx.x & 63) == 0) part[wave] = v;
+  barrier_keep_loads();
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) t += part[i];
+  return t;
+}
+
+// ------------------------------------------------------------------ forward
+
+// WPR waves to a row, CH chunks of 8 elements per lane; workgroups walk over the rows.
+template <bool BF16, int WPR, int CH>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs a) {
+  constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, RPB = WPR > 4 ? 1 : 4 / WPR;
+  __shared__ float part[RPB][2][WPR];
+  const int lane = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  float w[CH][8], b[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_param(a.weight, a.par_bf16, (c * LPR + lane) * 8, a.H, 1.f, w[c]);
+    load_param(a.bias, a.par_bf16, (c * LPR + lane) * 8, a.H, 0.f, b[c]);
+  }
+  const float inv = 1.f / (float)a.H;
+  int parity = 0;
+  // (the workgroup's waves stay together for the barriers: a team without a row repeats the last one)
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
+    const bool mine = r0 + team < a.rows;
+    const long long r = mine ? r0 + team : a.rows - 1;
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+    Raw<BF16> raw[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) raw[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
+    float v[CH][8];
+    float mean = 0.f, sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      unpack<BF16>(raw[c], (c * LPR + lane) * 8, a.H, v[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[c][i];
+    }
+    if (!a.rms) mean = row_sum<WPR>(sum, part[team][parity]) * inv, parity ^= 1;
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = (c * LPR + lane) * 8 + i < a.H ? v[c][i] - mean : 0.f;
+        sq = fmaf(v[c][i], v[c][i], sq);
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<WPR>(sq, part[team][parity]) * inv + a.eps);
+    parity ^= 1;
+    if (!mine) continue;
+    char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i] * rstd, w[c][i], b[c][i]);
+      store_chunk<BF16>(yr, (c * LPR + lane) * 8, a.H, v[c]);
+    }
+    if (a.stats && lane == 0) a.stats[2 * r] = mean, a.stats[2 * r + 1] = rstd;
+  }
+}
+
+// Rows too long for the registers: the row is read again for every sum and for the result (from L2, as it was just read).
+template <bool BF16>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+  constexpr int LPR = 1024, EB = BF16 ? 2 : 4;
+  __shared__ float part[2][16];
+  const int lane = threadIdx.x;
+  const float inv = 1.f / (float)a.H;
+  int parity = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+    char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
+    float v[8], w[8], b[8], mean = 0.f, sum = 0.f, sq = 0.f;
+    if (!a.rms) {
+      for (int j = lane * 8; j < a.H; j += LPR * 8) {
+        unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += v[i];
+      }
+      mean = row_sum<16>(sum, part[parity]) * inv, parity ^= 1;
+    }
+    for (int j = lane * 8; j < a.H; j += LPR * 8) {
+      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = j + i < a.H ? v[i] - mean : 0.f;
+        sq = fmaf(d, d, sq);
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<16>(sq, part[parity]) * inv + a.eps);
+    parity ^= 1;
+    for (int j = lane * 8; j < a.H; j += LPR * 8) {
+      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+      load_param(a.weight, a.par_bf16, j, a.H, 1.f, w);
+      load_param(a.bias, a.par_bf16, j, a.H, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - mean) * rstd, w[i], b[i]);
+      store_chunk<BF16>(yr, j, a.H, v);
+    }
+    if (a.stats && lane == 0) a.stats[2 * r] = mean, a.stats[2 * r + 1] = rstd;
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+
+// dx of 8 elements, from the row's sums m1 and m2 (divided by H)
+template <bool BF16>
+__device__ __forceinline__ void write_dx(const NormArgs& a, long long r, int j, const float (&v)[8], const float (&xh)[8],
+                                         float m1, float m2, float rstd) {
+  constexpr int EB = BF16 ? 2 : 4;
+  const size_t at = (size_t)r * a.H * EB;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = rstd * (v[i] - m1 - xh[i] * m2);
+  if (a.add) {
+    float d[8];
+    unpack<BF16>(load_raw<BF16>((const char*)a.add + at, j, a.H), j, a.H, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] += d[i];
+  }
+  store_chunk<BF16>((char*)a.dx + at, j, a.H, o);
+}
+
+// 1024 threads: 16 / WPR teams of WPR waves, a row to a team at a time.
+template <bool BF16, int WPR, int CH>
+__global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
+  constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, TEAMS = 16 / WPR;
+  extern __shared__ float lds[];  // [2][H] sums of the workgroup's teams (TEAMS > 1)
+  __shared__ float part[TEAMS][2][2][WPR];
+  const int lane = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_param(a.weight, a.par_bf16, (c * LPR + lane) * 8, a.H, 1.f, w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.f;
+  }
+  const float inv = 1.f / (float)a.H;
+  int parity = 0;
+  for (long long r0 = (long long)blockIdx.x * TEAMS; r0 < a.rows; r0 += (long long)gridDim.x * TEAMS) {
+    const bool mine = r0 + team < a.rows;
+    const long long r = mine ? r0 + team : a.rows - 1;
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+    const char* dr = (const char*)a.dy + (size_t)r * a.ldy * EB;
+    const float mean = a.rms ? 0.f : a.stats[2 * r], rstd = a.stats[2 * r + 1];
+    Raw<BF16> rx[CH], rd[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      rx[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
+      rd[c] = load_raw<BF16>(dr, (c * LPR + lane) * 8, a.H);
+    }
+    float v[CH][8], xh[CH][8];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * LPR + lane) * 8;
+      float d[8];
+      unpack<BF16>(rx[c], j, a.H, xh[c]);
+      unpack<BF16>(rd[c], j, a.H, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xh[c][i] = (xh[c][i] - mean) * rstd;  // (past the row's end d and w are zeros)
+        v[c][i] = d[i] * w[c][i];
+        s1 += v[c][i];
+        s2 = fmaf(v[c][i], xh[c][i], s2);
+        if (mine) dw[c][i] = fmaf(d[i], xh[c][i], dw[c][i]), db[c][i] += d[i];
+      }
+    }
+    float m1 = 0.f, m2;
+    if constexpr (WPR == 1) {
+      m1 = wave_sum(s1), m2 = wave_sum(s2);
+    } else {
+      s1 = wave_sum(s1), s2 = wave_sum(s2);
+      const int wave = threadIdx.x / 64 % WPR;
+      float(&p)[2][WPR] = part[team][parity];
+      parity ^= 1;
+      if ((threadIdx.x & 63) == 0) p[0][wave] = s1, p[1][wave] = s2;
+      barrier_keep_loads();
+      m2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) m1 += p[0][i], m2 += p[1][i];
+    }
+    m1 = a.rms ? 0.f : m1 * inv, m2 *= inv;
+    if (!mine) continue;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if ((c * LPR + lane) * 8 < a.H) write_dx<BF16>(a, r, (c * LPR + lane) * 8, v[c], xh[c], m1, m2, rstd);
+  }
+  if (!a.part) return;
+  float* out = a.part + (size_t)blockIdx.x * 2 * a.H;
+  if constexpr (TEAMS == 1) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      store_chunk<false>(out, (c * LPR + lane) * 8, a.H, dw[c]);
+      store_chunk<false>(out + a.H, (c * LPR + lane) * 8, a.H, db[c]);
+    }
+  } else {
+    // team after team adds its sums to the workgroup's
+    for (int t = 0; t < TEAMS; ++t) {
+      if (team == t) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = (c * LPR + lane) * 8 + i;
+            if (j >= a.H) continue;
+            lds[j] = t ? lds[j] + dw[c][i] : dw[c][i];
+            lds[a.H + j] = t ? lds[a.H + j] + db[c][i] : db[c][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (int j = threadIdx.x; j < 2 * a.H; j += 1024) out[j] = lds[j];
+  }
+}
+
+// Rows too long for the registers: a kernel for the rows' sums, and one over columns for dx and the sums over rows.
+template <bool BF16>
+__global__ __launch_bounds__(1024) void norm_grad_sums_kernel(NormArgs a) {
+  constexpr int LPR = 1024, EB = BF16 ? 2 : 4;
+  __shared__ float part[2][2][16];
+  const int lane = threadIdx.x;
+  int parity = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+    const char* dr = (const char*)a.dy + (size_t)r * a.ldy * EB;
+    const float mean = a.rms ? 0.f : a.stats[2 * r], rstd = a.stats[2 * r + 1];
+    float x[8], d[8], w[8], s1 = 0.f, s2 = 0.f;
+    for (int j = lane * 8; j < a.H; j += LPR * 8) {
+      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, x);
+      unpack<BF16>(load_raw<BF16>(dr, j, a.H), j, a.H, d);
+      load_param(a.weight, a.par_bf16, j, a.H, 1.f, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = d[i] * w[i];
+        s1 += v;
+        s2 = fmaf(v, (x[i] - mean) * rstd, s2);
+      }
+    }
+    s1 = row_sum<16>(s1, part[parity][0]);
+    s2 = row_sum<16>(s2, part[parity][1]);
+    parity ^= 1;
+    if (lane == 0) a.sums[2 * r] = a.rms ? 0.f : s1 / (float)a.H, a.sums[2 * r + 1] = s2 / (float)a.H;
+  }
+}
+template <bool BF16>
+__global__ __launch_bounds__(256) void norm_grad_columns_kernel(NormArgs a) {
+  constexpr int EB = BF16 ? 2 : 4;
+  const int j = (blockIdx.x * 256 + threadIdx.x) * 8;
+  if (j >= a.H) return;
+  float w[8], dw[8] = {}, db[8] = {};
+  load_param(a.weight, a.par_bf16, j, a.H, 1.f, w);
+  for (long long r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    const float mean = a.rms ? 0.f : a.stats[2 * r], rstd = a.stats[2 * r + 1];
+    float x[8], d[8], v[8];
+    unpack<BF16>(load_raw<BF16>((const char*)a.x + (size_t)r * a.ldx * EB, j, a.H), j, a.H, x);
+    unpack<BF16>(load_raw<BF16>((const char*)a.dy + (size_t)r * a.ldy * EB, j, a.H), j, a.H, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = (x[i] - mean) * rstd;
+      v[i] = d[i] * w[i];
+      dw[i] = fmaf(d[i], x[i], dw[i]), db[i] += d[i];
+    }
+    write_dx<BF16>(a, r, j, v, x, a.sums[2 * r], a.sums[2 * r + 1], rstd);
+  }
+  if (!a.part) return;
+  float* out = a.part + (size_t)blockIdx.y * 2 * a.H;
+  store_chunk<false>(out, j, a.H, dw);
+  store_chunk<false>(out + a.H, j, a.H, db);
+}
+
+// dweight and dbias from the parts: a workgroup adds up 64 columns, its 16 waves every 16th part each, then the waves' sums
+// in order.
+__global__ __launch_bounds__(1024) void norm_parts_kernel(const float* __restrict__ part, int parts, int H, int par_bf16,
+                                                          void* __restrict__ dweight, void* __restrict__ dbias) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane, which = blockIdx.y;
+  void* out = which ? dbias : dweight;
+  if (!out) return;
+  float v = 0.f;
+  if (col < H)
+    for (int p = wave; p < parts; p += 16) v += part[((size_t)p * 2 + which) * H + col];
+  sum[wave][lane] = v;
+  __syncthreads();
+  if (wave || col >= H) return;
+  for (int i = 1; i < 16; ++i) v += sum[i][lane];
+  if (par_bf16) ((unsigned short*)out)[col] = f32_to_bf16_rne(v);
+  else ((float*)out)[col] = v;
+}
+
+template <bool BF16>
+int norm_any(const NormArgs& a, hipStream_t s) {
+  auto go = [&](auto wpr, auto ch) {
+    constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value, RPB = WPR > 4 ? 1 : 4 / WPR;
+    const int threads = WPR > 4 ? 64 * WPR : 256;
+    const long long blocks = ((long long)a.rows + RPB - 1) / RPB, slots = (long long)cu_count() * (2048 / threads);
+    hipLaunchKernelGGL((norm_kernel<BF16, WPR, CH>), dim3((unsigned)std::min(blocks, slots)), dim3(threads), 0, s, a);
+  };
+  using std::integral_constant;
+#define MOE_NORM(W, C) go(integral_constant<int, W>{}, integral_constant<int, C>{})
+  if (a.H <= 512) MOE_NORM(1, 1);
+  else if (a.H <= 1024) MOE_NORM(1, 2);
+  else if (a.H <= 2048) MOE_NORM(4, 1);
+  else if (a.H <= 4096) MOE_NORM(4, 2);
+  else if (a.H <= 8192) MOE_NORM(16, 1);
+  else if (a.H <= 16384) MOE_NORM(16, 2);
+  else
+    hipLaunchKernelGGL(norm_long_kernel<BF16>, dim3((unsigned)std::min((long long)a.rows, 2LL * cu_count())), dim3(1024), 0, s,
+                       a);
+#undef MOE_NORM
+  MOE_CHECK_LAUNCH("moe_norm launch");
+  return MOE_OK;
+}
+
+template <bool BF16>
+int norm_grad_any(const NormArgs& a, hipStream_t s) {
+  const int parts = norm_parts(a.rows, a.H);  // (none without rows: the sums over them are zeros)
+  auto go = [&](auto wpr, auto ch) {
+    constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
+    const size_t lds = WPR < 16 ? (size_t)a.H * 8 : 0;
+    hipLaunchKernelGGL((norm_grad_kernel<BF16, WPR, CH>), dim3(parts), dim3(1024), lds, s, a);
+  };
+  using std::integral_constant;
+#define MOE_NORM(W, C) go(integral_constant<int, W>{}, integral_constant<int, C>{})
+  if (a.rows == 0) {}
+  else if (a.H <= 512) MOE_NORM(1, 1);
+  else if (a.H <= 1024) MOE_NORM(2, 1);
+  else if (a.H <= 2048) MOE_NORM(4, 1);
+  else if (a.H <= 4096) MOE_NORM(8, 1);
+  else if (a.H <= 8192) MOE_NORM(16, 1);
+  else if (a.H <= 16384) MOE_NORM(16, 2);
+  else {
+    hipLaunchKernelGGL(norm_grad_sums_kernel<BF16>, dim3((unsigned)std::min((long long)a.rows, 2LL * cu_count())), dim3(1024),
+                       0, s, a);
+    hipLaunchKernelGGL(norm_grad_columns_kernel<BF16>, dim3((a.H + 2047) / 2048, parts), dim3(256), 0, s, a);
+  }
+#undef MOE_NORM
+  MOE_CHECK_LAUNCH("moe_norm_grad launch");
+  if (a.dweight || a.dbias) {
+    hipLaunchKernelGGL(norm_parts_kernel, dim3((a.H + 63) / 64, a.dbias ? 2 : 1), dim3(1024), 0, s, a.part, parts, a.H,
+                       a.par_bf16, a.dweight, a.dbias);
+    MOE_CHECK_LAUNCH("moe_norm_grad launch");
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+bool norm_long(int H) { return H > 16384; }
+
+// One workgroup of 1024 threads to a compute unit, or fewer where there are fewer rows; long rows: as many parts as give the
+// columns' kernel 1024 workgroups.
+int norm_parts(int rows, int H) {
+  if (rows < 1) return 0;
+  if (norm_long(H)) return std::min(rows, std::max(1, 1024 / ((H + 2047) / 2048)));
+  int teams = 16;
+  while (teams > 1 && 8192 / teams < H) teams /= 2;
+  return std::min((rows + teams - 1) / teams, cu_count());
+}
+
+int launch_norm(const NormArgs& a, int dt, hipStream_t s) { return dt == MOE_BF16 ? norm_any<true>(a, s) : norm_any<false>(a, s); }
+
+int launch_norm_grad(const NormArgs& a, int dt, hipStream_t s) {
+  return dt == MOE_BF16 ? norm_grad_any<true>(a, s) : norm_grad_any<false>(a, s);
+}
+
+}  // namespace moe
