@@ -516,7 +516,7 @@ int moe_norm_grad(const moe_norm_desc* d, const void* dy, const void* x, const v
  *   norm  device, one fp32 (out)
  *   ws    moe_grad_norm_workspace bytes (device, 256-byte aligned); one call at a time may use it
  * dst may be src.  A dst that overlaps anything else in the list is refused, a gradient named twice in place among them.
- * Errors: MOE_ERR_INVALID (n out of 0..1<<16, null or misaligned pointers, bad types, numel out of 0..1<<40, overlaps,
+ * Errors: MOE_ERR_INVALID (n out of 0..1<<16, null or misaligned pointers, bad types, negative numel, more than 1<<40 elements, overlaps,
  * max_norm not positive and finite), MOE_ERR_WORKSPACE.
  */
 typedef struct {
@@ -526,7 +526,7 @@ typedef struct {
   int dt;
 } moe_tensor;
 
-size_t moe_grad_norm_workspace(const moe_tensor* t, int n);
+size_t moe_grad_norm_workspace(int n);
 int moe_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, size_t ws_bytes, void* stream);
 int moe_clip_grad_norm(const moe_tensor* t, int n, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream);
 

@@ -95,7 +95,7 @@ SIGNATURES = {
     "moe_norm": ([ctypes.POINTER(MoeNormDesc), vp, vp, vp, vp, f32p, vp], c_int),
     "moe_norm_workspace": ([c_int, c_int], c_size_t),
     "moe_norm_grad": ([ctypes.POINTER(MoeNormDesc), vp, vp, vp, f32p, vp, vp, vp, vp, vp, c_size_t, vp], c_int),
-    "moe_grad_norm_workspace": ([vp, c_int], c_size_t),  # (moe_tensor lists: any buffer of that layout)
+    "moe_grad_norm_workspace": ([c_int], c_size_t),
     "moe_grad_norm": ([vp, c_int, f32p, vp, c_size_t, vp], c_int),
     "moe_clip_grad_norm": ([vp, c_int, ctypes.c_float, f32p, vp, c_size_t, vp], c_int),
     "moe_combine_grad": ([vp, c_int, f32p, f32p, i32p, c_int, c_int, c_int, vp, c_int, f32p, i32p, c_int, f32p, vp],

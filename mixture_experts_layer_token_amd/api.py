@@ -460,30 +460,56 @@ def _is_dense(t):
     return True
 
 
+_DT_OF = {torch.float32: DT["f32"], torch.bfloat16: DT["bf16"]}
+
+
 def _tensor_list(grads, outs):
-    """moe_tensor entries of a list of gradients and of where their results go (an array of four 64-bit words each)."""
-    words = array.array("q")
-    for i, g in enumerate(grads):
-        if not g.is_cuda or not _is_dense(g):
-            raise ValueError("gradient %d: a device tensor without gaps expected" % i)
-        o = None if outs is None else outs[i]
-        if o is not None and (o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() or not o.is_cuda):
-            raise ValueError("result %d does not have its gradient's type, shape and strides" % i)
-        words.extend((g.data_ptr(), 0 if o is None else o.data_ptr(), g.numel(), _dt(g)))
-    return words
+    """moe_tensor entries of a list of gradients and of where their results go (four 64-bit words each), and their device.  Column
+    by column: a list of hundreds of tensors costs more time here than on the GPU."""
+    devices = {g.get_device() for g in grads}
+    numel = [g.numel() for g in grads]
+    try:
+        types = [_DT_OF[g.dtype] for g in grads]
+    except KeyError as e:
+        raise TypeError("gradients must be float32 or bfloat16, got %s" % e.args[0])
+    if not all([g.is_contiguous() for g in grads]) and not all(map(_is_dense, grads)):
+        raise ValueError("gradients without gaps expected")
+    src = [g.data_ptr() for g in grads]
+    if outs is None:
+        dst = [0] * len(src)
+    elif outs is grads:
+        dst = src
+    else:
+        dst = [0 if o is None else o.data_ptr() for o in outs]
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o is None:
+                continue
+            if o.dtype is not g.dtype or o.shape != g.shape or not (
+                    o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride()):
+                raise ValueError("result %d does not have its gradient's type, shape and strides" % i)
+            if o.get_device() not in devices:
+                raise ValueError("result %d is on another device" % i)
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError("gradients on one GPU expected")
+    words = array.array("q", bytes(32 * len(src)))
+    words[0::4], words[1::4] = array.array("q", src), array.array("q", dst)
+    words[2::4], words[3::4] = array.array("q", numel), array.array("q", types)
+    return words, devices
 
 
 def _grad_norm(f, grads, outs, args, norm, ws, stream):
     _need(norm, torch.float32, (1,), "norm")
-    words = _tensor_list(grads, outs)
-    at, n = words.buffer_info()[0], len(grads)
-    ws, wp, wn = _own_ws(ws, lambda: int(lib().moe_grad_norm_workspace(at, n)), norm.device, stream)
-    _launch(f, (at, n, *args, _ptr(norm), wp, wn), (norm, ws, *grads, *(outs or ())), stream)
+    words, devices = _tensor_list(grads, outs)
+    if devices and norm.get_device() not in devices:
+        raise ValueError("norm on device %d, gradients on another" % norm.get_device())
+    n = len(grads)
+    ws, wp, wn = _own_ws(ws, lambda: moe_grad_norm_workspace(n), norm.device, stream)
+    _launch(f, (words.buffer_info()[0], n, *args, _ptr(norm), wp, wn), (norm, ws), stream)
 
 
-def moe_grad_norm_workspace(grads) -> int:
-    words = _tensor_list(grads, None)
-    return int(lib().moe_grad_norm_workspace(words.buffer_info()[0], len(grads)))
+def moe_grad_norm_workspace(n) -> int:
+    """Workspace bytes for a list of n gradients."""
+    return int(lib().moe_grad_norm_workspace(n))
 
 
 def moe_grad_norm(grads, norm, ws=None, stream=None):

@@ -2,7 +2,7 @@
 // Bound by memory: the gradients are read for the sum, and read again and written for the result.
 //
 // The table of tensors travels as a kernel argument (nothing is copied to the device, so a call can be captured), kTensors to
-// a launch.  Tensors are cut into chunks of kChunk elements; a workgroup of the first kernel adds up the squares of every
+// a launch.  Tensors are cut into chunks; a workgroup of the first kernel adds up the squares of every
 // G-th chunk in 64 bits (they cost less than the bytes, the sum is as good as exact, and no square overflows) and leaves one
 // partial sum; every workgroup of the second adds those up in the same order, so all of them scale by the same number and
 // results are bitwise reproducible.
@@ -15,21 +15,25 @@
 namespace moe {
 namespace {
 
-constexpr int kTensors = 96, kChunk = 8192, kThreads = 256;
-constexpr int kBlocks = 2048;  // 8 to a compute unit
+constexpr int kTensors = 140, kThreads = 256;
+constexpr int kStep = kThreads * 8;      // elements of one pass of a workgroup
+constexpr int kUnroll = 4;               // passes whose loads are in flight together
+constexpr int kBlocks = 2048;            // 8 to a compute unit
+constexpr int kMaxChunk = kStep * 16;
 
 struct TensorTable {
   int n, chunks;
-  int end[kTensors];  // chunks of the tensors up to this one
-  int bf16[kTensors];
-  long long numel[kTensors];
+  int chunk;                  // elements
+  int end[kTensors];          // chunks of the tensors up to this one
+  long long numel[kTensors];  // complemented for bf16
   const void* src[kTensors];
-  void* dst[kTensors];  // null: not written
+  void* dst[kTensors];        // null: not written
 };
-static_assert(sizeof(TensorTable) <= 3500, "kernel argument");
+static_assert(sizeof(TensorTable) + 32 <= 4096, "kernel arguments");
 
 struct Chunk {
   int t, len;       // tensor, elements
+  bool bf16;
   long long first;  // its first element
 };
 __device__ __forceinline__ Chunk find_chunk(const TensorTable& tab, int c) {
@@ -39,14 +43,62 @@ __device__ __forceinline__ Chunk find_chunk(const TensorTable& tab, int c) {
     if (tab.end[mid] > c) hi = mid;
     else lo = mid + 1;
   }
-  const long long first = (long long)(c - (lo ? tab.end[lo - 1] : 0)) * kChunk;
-  return Chunk{lo, (int)min((long long)kChunk, tab.numel[lo] - first), first};
+  const long long first = (long long)(c - (lo ? tab.end[lo - 1] : 0)) * tab.chunk, n = tab.numel[lo];
+  return Chunk{lo, (int)min((long long)tab.chunk, (n < 0 ? ~n : n) - first), n < 0, first};
 }
 
+// Elements i .. i+7 of a chunk, at any element-aligned address.
 template <bool BF16>
-__device__ __forceinline__ float element(const void* p, long long i) {
-  if constexpr (BF16) return bf16_to_f32(((const unsigned short*)p)[i]);
-  return ((const float*)p)[i];
+struct Eight {
+  u32x4 v[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(gptr p, int i) {
+    v[0] = load_any(p + (size_t)i * (BF16 ? 2 : 4));
+    if constexpr (!BF16) v[1] = load_any(p + (size_t)i * 4 + 16);
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (BF16) return __uint_as_float(e % 2 ? v[0][e / 2] & 0xFFFF0000u : v[0][e / 2] << 16);
+    return __uint_as_float(v[e / 4][e % 4]);
+  }
+};
+template <bool BF16>
+__device__ __forceinline__ float element(gptr p, int i) {
+  if constexpr (BF16) return bf16_to_f32(((const __attribute__((address_space(1))) unsigned short*)p)[i]);
+  return ((const __attribute__((address_space(1))) float*)p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void store_eight(char* p, int i, const float (&v)[8]) {
+  typedef u32x4 __attribute__((aligned(1))) any4;
+  typedef __attribute__((address_space(1))) any4* anyp;
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 b2;
+  const anyp o = (anyp)((__attribute__((address_space(1))) char*)p + (size_t)i * (BF16 ? 2 : 4));
+  if constexpr (BF16) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(unsigned, b2{(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
+    *o = w;
+  } else {
+    o[0] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+    o[1] = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+  }
+}
+// f(i, eight) for the thread's groups of 8 elements of a chunk, kUnroll passes' loads together, then g(i) for the elements
+// behind the last whole group
+template <bool BF16, typename F, typename G>
+__device__ __forceinline__ void walk(gptr p, int len, F&& f, G&& g) {
+  int i = threadIdx.x * 8;
+  for (; i + (kUnroll - 1) * kStep + 8 <= len; i += kUnroll * kStep) {
+    Eight<BF16> x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x[u].load(p, i + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) f(i + u * kStep, x[u]);
+  }
+  for (; i + 8 <= len; i += kStep) {
+    Eight<BF16> x;
+    x.load(p, i);
+    f(i, x);
+  }
+  for (; i < len; ++i) g(i);  // (at most one thread, at most 7 elements: the chunk's end)
 }
 
 // the workgroup's sum, to every thread
@@ -62,21 +114,28 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 
 __global__ __launch_bounds__(kThreads) void square_sums_kernel(TensorTable tab, double* __restrict__ part) {
   __shared__ double lds[kThreads / 64];
-  double v = 0.0;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
   for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     const Chunk k = find_chunk(tab, c);
     auto add = [&](auto bf) {
       constexpr bool BF = decltype(bf)::value;
-      for (int i = threadIdx.x; i < k.len; i += kThreads) {
-        const double g = element<BF>(tab.src[k.t], k.first + i);
-        v = fma(g, g, v);
-      }
+      const gptr p = (gptr)tab.src[k.t] + k.first * (BF ? 2 : 4);
+      walk<BF>(p, k.len, [&](int, const Eight<BF>& x) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const double g = x.get(e);
+          v[e % 4] = fma(g, g, v[e % 4]);
+        }
+      }, [&](int i) {
+        const double g = element<BF>(p, i);
+        v[0] = fma(g, g, v[0]);
+      });
     };
-    if (tab.bf16[k.t]) add(std::true_type{});
+    if (k.bf16) add(std::true_type{});
     else add(std::false_type{});
   }
-  v = block_sum(v, lds);
-  if (threadIdx.x == 0) part[blockIdx.x] = v;
+  const double sum = block_sum((v[0] + v[1]) + (v[2] + v[3]), lds);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 // parts: of all tables of the call.  A norm that is not finite scales nothing.
@@ -84,7 +143,13 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable tab, const d
                                                         float max_norm, float* __restrict__ norm) {
   __shared__ double lds[kThreads / 64];
   double total = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) total += part[i];
+  for (int i = threadIdx.x; i < parts; i += 8 * kThreads) {  // (loads together)
+    double v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = part[min(i + u * kThreads, parts - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) total += i + u * kThreads < parts ? v[u] : 0.0;
+  }
   const double n = sqrt(block_sum(total, lds));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   if (!clip) return;
@@ -92,68 +157,81 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable tab, const d
   // (a factor that fp32 holds with fewer bits is applied in two: gradients near the end of the fp32 range have a norm past it)
   const float post = f < 0x1p-100 ? 0x1p-80f : 1.f;
   const float scale = (float)(f < 0x1p-100 ? f * 0x1p80 : f);
-  for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
+  // from the end: what the first kernel read last is still in the last-level cache
+  for (int c = tab.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const Chunk k = find_chunk(tab, c);
-    const void* src = tab.src[k.t];
-    void* dst = tab.dst[k.t];
-    if (!dst || (dst == src && f == 1.0)) continue;
+    if (!tab.dst[k.t] || (tab.dst[k.t] == tab.src[k.t] && f == 1.0)) continue;
     auto apply = [&](auto bf) {
       constexpr bool BF = decltype(bf)::value;
-      for (int i = threadIdx.x; i < k.len; i += kThreads) {
-        const float g = element<BF>(src, k.first + i) * scale * post;
-        if constexpr (BF) ((unsigned short*)dst)[k.first + i] = f32_to_bf16_rne(g);
-        else ((float*)dst)[k.first + i] = g;
-      }
+      const gptr p = (gptr)tab.src[k.t] + k.first * (BF ? 2 : 4);
+      char* o = (char*)tab.dst[k.t] + k.first * (BF ? 2 : 4);
+      walk<BF>(p, k.len, [&](int i, const Eight<BF>& x) {
+        float g[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = x.get(e) * scale * post;
+        store_eight<BF>(o, i, g);
+      }, [&](int i) {
+        const float g = element<BF>(p, i) * scale * post;
+        if constexpr (BF) ((unsigned short*)o)[i] = f32_to_bf16_rne(g);
+        else ((float*)o)[i] = g;
+      });
     };
-    if (tab.bf16[k.t]) apply(std::true_type{});
+    if (k.bf16) apply(std::true_type{});
     else apply(std::false_type{});
   }
 }
 
-long long chunks_of(const moe_tensor& t) { return (t.numel + kChunk - 1) / kChunk; }
+// Elements of a chunk: long ones cost less to find, short ones fill the card when there is little to do.
+int chunk_elements(const moe_tensor* t, int n) {
+  long long total = 0;
+  for (int i = 0; i < n; ++i) total += t[i].numel;
+  int chunk = kStep;
+  while (chunk < kMaxChunk && total / chunk > 4 * kBlocks) chunk *= 2;
+  return chunk;
+}
 
-// the next table's worth of tensors from `at` on (empty ones left out); at moves past them
-TensorTable next_table(const moe_tensor* t, int n, int& at) {
-  TensorTable tab = {};
-  for (; at < n && tab.n < kTensors; ++at) {
+// Tables of the call: as few as hold it, of about equal length.
+int tables_of(int n) { return (n + kTensors - 1) / kTensors; }
+// the next table of tensors from `at` on (empty ones left out); at moves past them
+void next_table(const moe_tensor* t, int n, int chunk, int& at, TensorTable& tab) {
+  tab.n = tab.chunks = 0, tab.chunk = chunk;
+  const int each = (n + std::max(tables_of(n), 1) - 1) / std::max(tables_of(n), 1);
+  for (const int end = std::min(n, at + each); at < end; ++at) {
     if (t[at].numel == 0) continue;
-    const long long c = chunks_of(t[at]);
-    if (tab.chunks + c > 0x7FFFFFFFLL) break;  // (one tensor alone always fits: numel is limited)
-    tab.chunks += (int)c;
+    tab.chunks += (int)((t[at].numel + chunk - 1) / chunk);
     tab.end[tab.n] = tab.chunks;
-    tab.bf16[tab.n] = t[at].dt == MOE_BF16;
-    tab.numel[tab.n] = t[at].numel;
+    tab.numel[tab.n] = t[at].dt == MOE_BF16 ? ~(long long)t[at].numel : t[at].numel;
     tab.src[tab.n] = t[at].src;
     tab.dst[tab.n] = t[at].dst;
     ++tab.n;
   }
-  return tab;
 }
 int blocks_of(const TensorTable& tab) { return std::min(tab.chunks, kBlocks); }
 
 }  // namespace
 
-size_t grad_norm_workspace(const moe_tensor* t, int n) {
-  long long parts = 0;
-  for (int at = 0; at < n;) parts += blocks_of(next_table(t, n, at));
-  return ((size_t)parts * sizeof(double) + 255) / 256 * 256 + 256;
-}
+size_t grad_norm_workspace(int n) { return ((size_t)std::max(tables_of(n), 1) * kBlocks * sizeof(double) + 255) / 256 * 256; }
 
 int launch_grad_norm(const moe_tensor* t, int n, int clip, float max_norm, float* norm, double* part, hipStream_t s) {
   int parts = 0;
+  const int chunk = chunk_elements(t, n);
+  TensorTable tab;
+  tab.n = tab.chunks = 0;
   for (int at = 0; at < n;) {
-    const TensorTable tab = next_table(t, n, at);
+    next_table(t, n, chunk, at, tab);
     if (!tab.n) continue;
     hipLaunchKernelGGL(square_sums_kernel, dim3(blocks_of(tab)), dim3(kThreads), 0, s, tab, part + parts);
     parts += blocks_of(tab);
   }
-  bool first = true;
-  for (int at = 0; first || (clip && at < n);) {
-    const TensorTable tab = next_table(t, n, at);
-    if (first || tab.n)
-      hipLaunchKernelGGL(clip_kernel, dim3(clip ? std::max(blocks_of(tab), 1) : 1), dim3(kThreads), 0, s, tab, part, parts, clip,
-                         max_norm, first ? norm : nullptr);
-    first = false;
+  // The norm comes with the first table that is scaled; the tables go backwards, for what the caches still hold.  (One table: it
+  // is there from above.)
+  const int tables = std::max(tables_of(n), 1), each = (n + tables - 1) / tables;
+  for (int i = tables - 1; i >= 0; --i) {
+    int at = i * each;
+    if (tables > 1) next_table(t, n, chunk, at, tab);
+    if (i < tables - 1 && (!clip || !tab.n)) continue;
+    hipLaunchKernelGGL(clip_kernel, dim3(clip ? std::max(blocks_of(tab), 1) : 1), dim3(kThreads), 0, s, tab, part, parts, clip,
+                       max_norm, i == tables - 1 ? norm : nullptr);
   }
   MOE_CHECK_LAUNCH("moe_clip_grad_norm launch");
   return MOE_OK;

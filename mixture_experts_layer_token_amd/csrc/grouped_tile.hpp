@@ -556,74 +556,118 @@ struct TileKernel {
     if constexpr (TYPE == kBf16) return __builtin_amdgcn_rcpf(1.f + __expf(-g));
     return 1.f / (1.f + expf(-g));
   }
-  // 4 neighbouring elements of a row of the operands' type
-  static __device__ __forceinline__ void store4(char* p, const float (&v)[4]) {
-    if constexpr (TYPE == kBf16) *(u32x2*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    else *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+  // 8 neighbouring elements of a row of the operands' type, in memory at any element-aligned address
+  struct Eight {
+    u32x4 v[EB / 2];
+    __device__ __forceinline__ void load(const char* base, unsigned off) {
+#pragma unroll
+      for (int h = 0; h < EB / 2; ++h) v[h] = load_any((gptr)base + off + 16 * h);
+    }
+    __device__ __forceinline__ float get(int e) const {
+      if constexpr (EB == 2) return __uint_as_float(e % 2 ? v[0][e / 2] & 0xFFFF0000u : v[0][e / 2] << 16);
+      return __uint_as_float(v[e / 4 % (EB / 2)][e % 4]);
+    }
+    static __device__ __forceinline__ void store(char* base, unsigned off, const float (&f)[8]) {
+      typedef u32x4 __attribute__((aligned(1))) any4;
+      const auto p = (__attribute__((address_space(1))) char*)base + off;
+      if constexpr (EB == 2) {
+        *(__attribute__((address_space(1))) any4*)p =
+            u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+      } else {
+        ((__attribute__((address_space(1))) any4*)p)[0] = __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]});
+        ((__attribute__((address_space(1))) any4*)p)[1] = __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]});
+      }
+    }
+  };
+  static __device__ __forceinline__ float load1(const char* p, size_t i) {
+    if constexpr (TYPE == kBf16) return bf16_to_f32(((const unsigned short*)p)[i]);
+    return ((const float*)p)[i];
+  }
+
+  // The gate's operands and results cross memory in rows: 16 rows of a wave's accumulators at a time pass through its own LDS
+  // region, so that a lane holds 8 neighbouring columns (16 bytes in bf16) and a row's lanes follow one another.  A row of the
+  // region is 4 WJ pieces of 4 columns, in the order in which the accumulators hold them, XORed by row against bank conflicts.
+  // One copy of the code behind the region serves all fragments of a tile: written out for each it spilled registers and
+  // waited for instructions (gradient at 6002 rows, 8 experts of 4096 x 14336: 870 -> 735 us; loads and stores in the
+  // accumulators' own layout 1074).
+  static __device__ __forceinline__ lptr piece(lptr reg, int row, int p) {
+    return reg + row * 64 * WJ + ((p ^ (row & (4 * WJ - 1))) << 4);
+  }
+  // straight from the accumulators, which the compiler would copy to vector registers first, all of them; the LDS serves a
+  // wave's instructions in order, so what is read from the region next is this
+  static __device__ __forceinline__ void acc_put(lptr p, const Acc& acc) {
+    asm volatile("ds_write_b128 %0, %1" : : "v"((unsigned)(size_t)p), "a"(acc) : "memory");
+  }
+  template <int NI>
+  static __device__ __forceinline__ void acc_to_region(lptr reg, int lane, const Acc (&acc)[WJ][NI], int i) {
+    static_for<NI>([&](auto ic) {
+      if (i == ic) {  // (uniform)
+#pragma unroll
+        for (int j = 0; j < WJ; ++j)
+          acc_put(piece(reg, lane & 15, 4 * j + (lane >> 4)), acc[j][ic]);
+      }
+    });
+  }
+  // columns 8 m .. 8 m + 7 of the region's row (GLU: of its gate (up 0) or up strips (up 1), which take turns)
+  static __device__ __forceinline__ void region_row(lptr reg, int row, int m, int up, float (&v)[8]) {
+    const int p = GLU ? 8 * (m / 2) + 2 * (m % 2) + 4 * up : 2 * m;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = *(const __attribute__((address_space(3))) f32x4*)piece(reg, row, p + h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
+    }
+  }
+  // column c of it
+  static __device__ __forceinline__ float region_one(lptr reg, int row, int c, int up) {
+    const int p = GLU ? c / 16 * 8 + 4 * up + c % 16 / 4 : c / 4;
+    return *(const __attribute__((address_space(3))) float*)(piece(reg, row, p) + c % 4 * 4);
   }
 
   // Results of the gated block: h = SiLU(g) u from the unrounded sums, and [g | u] itself if it is kept.
   template <int NI>
   static __device__ __forceinline__ void write_glu(const GroupArgs& a, const TileItem& t, const Feed& feed, Acc (&acc)[WJ][NI]) {
     const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
-    const int rlane = wi * 16 + (lane & 15), clane = WJ / 2 * wj * 16 + (lane >> 4) * 4;  // as in body()
-    const bool keep = a.gu != nullptr;
     const long long ldg = 2LL * a.N;
+    const int c0 = WJ * 8 * wj;  // the wave's first column
     char* h = (char*)a.y + ((size_t)t.p0 * a.ldy + t.j0) * EB;
-    char* gu = (char*)a.gu + ((size_t)t.p0 * ldg + t.j0) * EB;
+    char* gu = a.gu ? (char*)a.gu + ((size_t)t.p0 * ldg + t.j0) * EB : nullptr;
+    // the next tile's first stages have landed before the first store: its loop need not wait for stores
     if constexpr (!STAGED) wait_loads<0>();
-    if (((size_t)h | (size_t)(a.ldy * EB)) % (4 * EB) == 0 && (size_t)a.gu % (4 * EB) == 0 && a.N % 4 == 0) {
-      auto rows = [&](auto kept) {
+    const lptr reg = feed.lds + NB * STAGE + wave * REGION;
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      const int r0 = 32 * i + wi * 16;
+      acc_to_region<NI>(reg, lane, acc, i);
+      if (a.N % 8 == 0) {
+        constexpr int RI = 64 / WJ;  // rows at a time: WJ lanes to a row of 8 WJ columns
+        const int m = lane % WJ, col = c0 + 8 * m;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int r = 32 * i + rlane;
-          if (r >= t.ni) continue;
-          char* p = h + ((size_t)r * a.ldy + clane) * EB;
-          char* q = gu + ((size_t)r * ldg + clane) * EB;
+        for (int k = 0; k < 16 / RI; ++k) {
+          const int rr = k * RI + lane / WJ, r = r0 + rr;
+          float g[8], u[8], v[8];
+          region_row(reg, rr, m, 0, g);
+          region_row(reg, rr, m, 1, u);
 #pragma unroll
-          for (int j = 0; j < WJ / 2; ++j) {
-            if (clane + 16 * j >= t.nj) continue;
-            float g[4], u[4], v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              g[e] = acc_get(acc[2 * j][i], e), u[e] = acc_get(acc[2 * j + 1][i], e);
-              v[e] = g[e] * sigmoid(g[e]) * u[e];
-            }
-            store4(p + 16 * j * EB, v);
-            if constexpr (decltype(kept)::value) {
-              store4(q + 16 * j * EB, g);
-              store4(q + ((size_t)a.N + 16 * j) * EB, u);
-            }
+          for (int e = 0; e < 8; ++e) v[e] = g[e] * sigmoid(g[e]) * u[e];
+          if (r >= t.ni || col >= t.nj) continue;
+          Eight::store(h + (size_t)r * a.ldy * EB, col * EB, v);  // (ldy may be anything; rows of gu end within 32 bits)
+          if (gu) {
+            const unsigned q = (unsigned)(r * (unsigned)ldg + col) * EB;
+            Eight::store(gu, q, g);
+            Eight::store(gu + (size_t)a.N * EB, q, u);
           }
         }
-      };
-      if (keep) rows(std::true_type{});
-      else rows(std::false_type{});
-    } else {
-      // any other: 16 rows at a time through the wave's own LDS region (g, then u behind it), element by element
-      typedef __attribute__((address_space(3))) float* lfloat;
-      constexpr int W = 16 * WJ / 2;
-      const lfloat reg = (lfloat)(feed.lds + NB * STAGE + wave * REGION);
-      const int c0 = WJ / 2 * wj * 16, nj = min(t.nj - c0, W);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-#pragma unroll
-        for (int j = 0; j < WJ; ++j) {
-          f32x4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc_get(acc[j][i], e);
-          *(__attribute__((address_space(3))) f32x4*)(reg + (j & 1) * 16 * W + (lane & 15) * W + j / 2 * 16 + (lane >> 4) * 4) = v;
-        }
-        const int r0 = 32 * i + wi * 16;
+      } else {
 #pragma unroll 1
         for (int r = 0; r < min(t.ni - r0, 16); ++r)
-#pragma unroll 1
-          for (int c = lane; c < nj; c += 64) {
-            const float g = reg[r * W + c], u = reg[(16 + r) * W + c];
-            store_out(h, (size_t)(r0 + r) * a.ldy + c0 + c, g * sigmoid(g) * u, EB == 2);
-            if (!keep) continue;
-            store_out(gu, (size_t)(r0 + r) * ldg + c0 + c, g, EB == 2);
-            store_out(gu, (size_t)(r0 + r) * ldg + a.N + c0 + c, u, EB == 2);
+          if (lane < min(t.nj - c0, 8 * WJ)) {  // (8 WJ <= 64 columns)
+            const float g = region_one(reg, r, lane, 0), u = region_one(reg, r, lane, 1);
+            store_out(h, (size_t)(r0 + r) * a.ldy + c0 + lane, g * sigmoid(g) * u, EB == 2);
+            if (gu) {
+              store_out(gu, (size_t)(r0 + r) * ldg + c0 + lane, g, EB == 2);
+              store_out(gu, (size_t)(r0 + r) * ldg + a.N + c0 + lane, u, EB == 2);
+            }
           }
       }
     }
@@ -631,88 +675,71 @@ struct TileKernel {
 
   // Results of the block's gradient: with dh the sums, s = 1 / (1 + e^-g),
   //   dgu = [dh u s (1 + g (1 - s)) | dh g s],  h = g s u
+  // The loads of the next 16 rows of [g | u] are under way while 16 rows are worked on.
   template <int NI>
   static __device__ __forceinline__ void write_glu_dx(const GroupArgs& a, const TileItem& t, const Feed& feed, Acc (&acc)[WJ][NI]) {
     const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
-    const int rlane = wi * 16 + (lane & 15), clane = WJ * wj * 16 + (lane >> 4) * 4;
     const long long ldg = 2LL * a.K;
-    const size_t o = ((size_t)t.p0 * ldg + t.j0) * EB;
+    const int c0 = WJ * 16 * wj;
+    const size_t o = ((size_t)t.p0 * ldg + t.j0) * EB, up = (size_t)a.K * EB;
     const char* gu = (const char*)a.gu + o;
     char* dgu = (char*)a.dgu + o;
-    char* h = (char*)a.h + ((size_t)t.p0 * a.K + t.j0) * EB;
-    auto grad = [](float dh, float g, float u, float& dg, float& du, float& hv) {
-      const float s = sigmoid(g);
-      dg = dh * u * s * (1.f + g * (1.f - s));
-      du = dh * g * s;
-      hv = g * s * u;
-    };
-    if constexpr (!STAGED) wait_loads<0>();
-    if (((size_t)a.gu | (size_t)a.dgu | (size_t)a.h) % (4 * EB) == 0 && a.K % 4 == 0) {
-      auto rows = [&](auto with_h) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int r = 32 * i + rlane;
-          if (r >= t.ni) continue;
-          const size_t q = ((size_t)r * ldg + clane) * EB;
-#pragma unroll
-          for (int j = 0; j < WJ; ++j) {
-            if (clane + 16 * j >= t.nj) continue;
-            float g[4], u[4], dg[4], du[4], hv[4];
-            load4(gu + q + 16 * j * EB, g);
-            load4(gu + q + ((size_t)a.K + 16 * j) * EB, u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) grad(acc_get(acc[j][i], e), g[e], u[e], dg[e], du[e], hv[e]);
-            store4(dgu + q + 16 * j * EB, dg);
-            store4(dgu + q + ((size_t)a.K + 16 * j) * EB, du);
-            if constexpr (decltype(with_h)::value) store4(h + ((size_t)r * a.K + clane + 16 * j) * EB, hv);
-          }
-        }
+    char* h = a.h ? (char*)a.h + ((size_t)t.p0 * a.K + t.j0) * EB : nullptr;
+    const lptr reg = feed.lds + NB * STAGE + wave * REGION;
+    if (a.K % 8 == 0) {
+      constexpr int LR = 2 * WJ, RI = 64 / LR, IT = 16 / RI;  // lanes to a row of 16 WJ columns, rows at a time
+      const int m = lane % LR, col = c0 + 8 * m;
+      const unsigned safe = min(col, t.nj - 8);  // (t.nj is a multiple of 8 as well)
+      Eight g[IT], u[IT];
+      auto fetch = [&](int i, int k) {
+        const unsigned r = min(32 * i + wi * 16 + k * RI + lane / LR, t.ni - 1), q = (r * (unsigned)ldg + safe) * EB;
+        g[k].load(gu, q);
+        u[k].load(gu + up, q);
       };
-      if (a.h) rows(std::true_type{});
-      else rows(std::false_type{});
-    } else {
-      typedef __attribute__((address_space(3))) float* lfloat;
-      constexpr int W = 16 * WJ;
-      const lfloat reg = (lfloat)(feed.lds + NB * STAGE + wave * REGION);
-      const int c0 = WJ * wj * 16, nj = min(t.nj - c0, W);
 #pragma unroll
+      for (int k = 0; k < IT; ++k) fetch(0, k);
+      if constexpr (!STAGED) wait_loads<0>();
+#pragma unroll 1
       for (int i = 0; i < NI; ++i) {
+        acc_to_region<NI>(reg, lane, acc, i);
 #pragma unroll
-        for (int j = 0; j < WJ; ++j) {
-          f32x4 v;
+        for (int k = 0; k < IT; ++k) {
+          const int rr = k * RI + lane / LR, r = 32 * i + wi * 16 + rr;
+          float dh[8], dg[8], du[8], hv[8];
+          region_row(reg, rr, m, 0, dh);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc_get(acc[j][i], e);
-          *(__attribute__((address_space(3))) f32x4*)(reg + (lane & 15) * W + 16 * j + (lane >> 4) * 4) = v;
+          for (int e = 0; e < 8; ++e) {
+            const float gv = g[k].get(e), uv = u[k].get(e), s = sigmoid(gv), gs = gv * s;
+            dg[e] = dh[e] * uv * (s * (1.f + gv * (1.f - s)));
+            du[e] = dh[e] * gs;
+            hv[e] = gs * uv;
+          }
+          fetch(min(i + 1, NI - 1), k);
+          if (r >= t.ni || col >= t.nj) continue;
+          const unsigned q = (r * (unsigned)ldg + col) * EB;
+          Eight::store(dgu, q, dg);
+          Eight::store(dgu + up, q, du);
+          if (h) Eight::store(h, (unsigned)(r * (unsigned)a.K + col) * EB, hv);
         }
+      }
+    } else {
+      if constexpr (!STAGED) wait_loads<0>();
+#pragma unroll 1
+      for (int i = 0; i < NI; ++i) {
+        acc_to_region<NI>(reg, lane, acc, i);
         const int r0 = 32 * i + wi * 16;
 #pragma unroll 1
         for (int r = 0; r < min(t.ni - r0, 16); ++r)
 #pragma unroll 1
-          for (int c = lane; c < nj; c += 64) {
+          for (int c = lane; c < min(t.nj - c0, 16 * WJ); c += 64) {
             const size_t q = (size_t)(r0 + r) * ldg + c0 + c;
-            float dg, du, hv;
-            grad(reg[r * W + c], load1(gu, q), load1(gu, q + a.K), dg, du, hv);
-            store_out(dgu, q, dg, EB == 2);
-            store_out(dgu, q + a.K, du, EB == 2);
-            if (a.h) store_out(h, (size_t)(r0 + r) * a.K + c0 + c, hv, EB == 2);
+            const float dh = region_one(reg, r, c, 0), gv = load1(gu, q), uv = load1(gu + up, q), s = sigmoid(gv), gs = gv * s;
+            store_out(dgu, q, dh * uv * (s * (1.f + gv * (1.f - s))), EB == 2);
+            store_out(dgu + up, q, dh * gs, EB == 2);
+            if (h) store_out(h, (size_t)(r0 + r) * a.K + c0 + c, gs * uv, EB == 2);
           }
       }
     }
-  }
-  static __device__ __forceinline__ void load4(const char* p, float (&v)[4]) {
-    if constexpr (TYPE == kBf16) {
-      const u32x2 b = *(const u32x2*)p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(e % 2 ? b[e / 2] & 0xFFFF0000u : b[e / 2] << 16);
-    } else {
-      const f32x4 b = *(const f32x4*)p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = b[e];
-    }
-  }
-  static __device__ __forceinline__ float load1(const char* p, size_t i) {
-    if constexpr (TYPE == kBf16) return bf16_to_f32(((const unsigned short*)p)[i]);
-    return ((const float*)p)[i];
   }
 
   // One tile with NI row fragments per wave.  Its first NB stages have landed for this wave (STAGED: feed is

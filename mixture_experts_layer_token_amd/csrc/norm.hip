@@ -145,12 +145,24 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 
 // ------------------------------------------------------------------ forward
 
-// WPR waves to a row, CH chunks of 8 elements per lane; workgroups walk over the rows.
+// WPR waves to a row, CH chunks of 8 elements per lane; workgroups walk over the rows, with the next row's loads under
+// way while one is worked on (a row's two sums each wait for all of its waves).
 template <bool BF16, int WPR, int CH>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs a) {
   constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, RPB = WPR > 4 ? 1 : 4 / WPR;
   __shared__ float part[RPB][2][WPR];
-  const int lane = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  const int lane = threadIdx.x % LPR, team = __builtin_amdgcn_readfirstlane(threadIdx.x / LPR);
+  const long long step = (long long)gridDim.x * RPB;
+  long long r0 = (long long)blockIdx.x * RPB;
+  Raw<BF16> raw[CH];
+  auto fetch = [&](long long first) {
+    const long long r = first + team;
+    if (r >= a.rows) return;  // (uniform over a wave)
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) raw[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
+  };
+  fetch(r0);
   float w[CH][8], b[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -159,14 +171,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
   }
   const float inv = 1.f / (float)a.H;
   int parity = 0;
-  // (the workgroup's waves stay together for the barriers: a team without a row repeats the last one)
-  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
-    const bool mine = r0 + team < a.rows;
-    const long long r = mine ? r0 + team : a.rows - 1;
-    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
-    Raw<BF16> raw[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) raw[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
+  // (the workgroup's waves stay together for the barriers, whether or not their team has a row)
+  for (; r0 < a.rows; r0 += step) {
     float v[CH][8];
     float mean = 0.f, sum = 0.f;
 #pragma unroll
@@ -175,6 +181,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += v[c][i];
     }
+    fetch(r0 + step);
     if (!a.rms) mean = row_sum<WPR>(sum, part[team][parity]) * inv, parity ^= 1;
     float sq = 0.f;
 #pragma unroll
@@ -187,7 +194,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
     }
     const float rstd = 1.f / sqrtf(row_sum<WPR>(sq, part[team][parity]) * inv + a.eps);
     parity ^= 1;
-    if (!mine) continue;
+    const long long r = r0 + team;
+    if (r >= a.rows) continue;
     char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -261,13 +269,36 @@ __device__ __forceinline__ void write_dx(const NormArgs& a, long long r, int j, 
   store_chunk<BF16>((char*)a.dx + at, j, a.H, o);
 }
 
-// 1024 threads: 16 / WPR teams of WPR waves, a row to a team at a time.
+// 1024 threads: 16 / WPR teams of WPR waves, a row to a team at a time, the next row's loads under way (one chunk per lane; two
+// leave no registers for that).
 template <bool BF16, int WPR, int CH>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
   constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, TEAMS = 16 / WPR;
-  extern __shared__ float lds[];  // [2][H] sums of the workgroup's teams (TEAMS > 1)
+  constexpr bool AHEAD = CH == 1;
+  __shared__ __align__(16) float lds[TEAMS > 1 ? 8192 : 1];
   __shared__ float part[TEAMS][2][2][WPR];
-  const int lane = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  const int lane = threadIdx.x % LPR, team = __builtin_amdgcn_readfirstlane(threadIdx.x / LPR);
+  const long long step = (long long)gridDim.x * TEAMS;
+  long long r0 = (long long)blockIdx.x * TEAMS;
+  struct Row {
+    Raw<BF16> x[CH], d[CH], a[AHEAD ? CH : 1];
+    float mean, rstd;
+  } row;
+  auto fetch = [&](long long first) {
+    const long long r = first + team;
+    if (r >= a.rows) return;  // (uniform over a wave)
+    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+    const char* dr = (const char*)a.dy + (size_t)r * a.ldy * EB;
+    row.mean = a.stats[2 * r], row.rstd = a.stats[2 * r + 1];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      row.x[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
+      row.d[c] = load_raw<BF16>(dr, (c * LPR + lane) * 8, a.H);
+      if constexpr (AHEAD)
+        if (a.add) row.a[c] = load_raw<BF16>((const char*)a.add + (size_t)r * a.H * EB, (c * LPR + lane) * 8, a.H);
+    }
+  };
+  if constexpr (AHEAD) fetch(r0);
   float w[CH][8], dw[CH][8], db[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -277,26 +308,20 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
   }
   const float inv = 1.f / (float)a.H;
   int parity = 0;
-  for (long long r0 = (long long)blockIdx.x * TEAMS; r0 < a.rows; r0 += (long long)gridDim.x * TEAMS) {
+  for (; r0 < a.rows; r0 += step) {
     const bool mine = r0 + team < a.rows;
-    const long long r = mine ? r0 + team : a.rows - 1;
-    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
-    const char* dr = (const char*)a.dy + (size_t)r * a.ldy * EB;
-    const float mean = a.rms ? 0.f : a.stats[2 * r], rstd = a.stats[2 * r + 1];
-    Raw<BF16> rx[CH], rd[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      rx[c] = load_raw<BF16>(xr, (c * LPR + lane) * 8, a.H);
-      rd[c] = load_raw<BF16>(dr, (c * LPR + lane) * 8, a.H);
-    }
-    float v[CH][8], xh[CH][8];
+    if constexpr (!AHEAD) fetch(r0);
+    float v[CH][8], xh[CH][8], o[8];
     float s1 = 0.f, s2 = 0.f;
+    const float mean = a.rms ? 0.f : row.mean, rstd = row.rstd;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * LPR + lane) * 8;
       float d[8];
-      unpack<BF16>(rx[c], j, a.H, xh[c]);
-      unpack<BF16>(rd[c], j, a.H, d);
+      unpack<BF16>(row.x[c], j, a.H, xh[c]);
+      unpack<BF16>(row.d[c], j, a.H, d);
+      if constexpr (AHEAD)
+        if (a.add) unpack<BF16>(row.a[c], j, a.H, o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xh[c][i] = (xh[c][i] - mean) * rstd;  // (past the row's end d and w are zeros)
@@ -306,6 +331,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
         if (mine) dw[c][i] = fmaf(d[i], xh[c][i], dw[c][i]), db[c][i] += d[i];
       }
     }
+    if constexpr (AHEAD) fetch(r0 + step);
     float m1 = 0.f, m2;
     if constexpr (WPR == 1) {
       m1 = wave_sum(s1), m2 = wave_sum(s2);
@@ -323,34 +349,47 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
     m1 = a.rms ? 0.f : m1 * inv, m2 *= inv;
     if (!mine) continue;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if ((c * LPR + lane) * 8 < a.H) write_dx<BF16>(a, r, (c * LPR + lane) * 8, v[c], xh[c], m1, m2, rstd);
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * LPR + lane) * 8;
+      if (j >= a.H) continue;
+      char* dr = (char*)a.dx + (size_t)(r0 + team) * a.H * EB;
+      if constexpr (!AHEAD)
+        if (a.add) unpack<BF16>(load_raw<BF16>((const char*)a.add + (size_t)(r0 + team) * a.H * EB, j, a.H), j, a.H, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = rstd * (v[c][i] - m1 - xh[c][i] * m2);
+        o[i] = a.add ? g + o[i] : g;
+      }
+      store_chunk<BF16>(dr, j, a.H, o);
+    }
   }
   if (!a.part) return;
   float* out = a.part + (size_t)blockIdx.x * 2 * a.H;
   if constexpr (TEAMS == 1) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      store_chunk<false>(out, (c * LPR + lane) * 8, a.H, dw[c]);
-      store_chunk<false>(out + a.H, (c * LPR + lane) * 8, a.H, db[c]);
+      if (a.dweight) store_chunk<false>(out, (c * LPR + lane) * 8, a.H, dw[c]);
+      if (a.dbias) store_chunk<false>(out + a.H, (c * LPR + lane) * 8, a.H, db[c]);
     }
   } else {
-    // team after team adds its sums to the workgroup's
-    for (int t = 0; t < TEAMS; ++t) {
-      if (team == t) {
+    // the teams' sums side by side in LDS (TEAMS * H <= 8192), added up column by column in team order; dw, then db
+    auto add_up = [&](const float(&v)[CH][8], float* to) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = (c * LPR + lane) * 8 + i;
-            if (j >= a.H) continue;
-            lds[j] = t ? lds[j] + dw[c][i] : dw[c][i];
-            lds[a.H + j] = t ? lds[a.H + j] + db[c][i] : db[c][i];
-          }
-      }
+        for (int i = 0; i < 8; ++i)
+          if ((c * LPR + lane) * 8 + i < a.H) lds[team * a.H + (c * LPR + lane) * 8 + i] = v[c][i];
       __syncthreads();
-    }
-    for (int j = threadIdx.x; j < 2 * a.H; j += 1024) out[j] = lds[j];
+      for (int j = threadIdx.x; j < a.H; j += 1024) {
+        float t = lds[j];
+#pragma unroll
+        for (int i = 1; i < TEAMS; ++i) t += lds[i * a.H + j];
+        to[j] = t;
+      }
+    };
+    if (a.dweight) add_up(dw, out);
+    if (a.dweight && a.dbias) __syncthreads();
+    if (a.dbias) add_up(db, out + a.H);
   }
 }
 
@@ -405,8 +444,8 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(NormArgs a) {
   }
   if (!a.part) return;
   float* out = a.part + (size_t)blockIdx.y * 2 * a.H;
-  store_chunk<false>(out, j, a.H, dw);
-  store_chunk<false>(out + a.H, j, a.H, db);
+  if (a.dweight) store_chunk<false>(out, j, a.H, dw);
+  if (a.dbias) store_chunk<false>(out + a.H, j, a.H, db);
 }
 
 // dweight and dbias from the parts: a workgroup adds up 64 columns, its 16 waves every 16th part each, then the waves' sums
@@ -419,8 +458,14 @@ __global__ __launch_bounds__(1024) void norm_parts_kernel(const float* __restric
   void* out = which ? dbias : dweight;
   if (!out) return;
   float v = 0.f;
-  if (col < H)
-    for (int p = wave; p < parts; p += 16) v += part[((size_t)p * 2 + which) * H + col];
+  // (the loads of 16 parts together: one after the other they are a chain of latencies)
+  for (int p0 = wave; p0 < parts; p0 += 16 * 16) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = part[((size_t)min(p0 + 16 * i, parts - 1) * 2 + which) * H + min(col, H - 1)];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += p0 + 16 * i < parts ? x[i] : 0.f;
+  }
   sum[wave][lane] = v;
   __syncthreads();
   if (wave || col >= H) return;
@@ -439,11 +484,15 @@ int norm_any(const NormArgs& a, hipStream_t s) {
   };
   using std::integral_constant;
 #define MOE_NORM(W, C) go(integral_constant<int, W>{}, integral_constant<int, C>{})
+  // Few rows: as many lanes as possible to each, one chunk per lane (one row of 7168: 16 waves 2.85 us, 8 waves of two chunks
+  // 3.2, 4 of four 4.5).  Many: fewer waves to wait for one another (8192 rows of 7168: 53, 40 and 45 us).
+  const bool few = a.rows <= 2 * cu_count();
   if (a.H <= 512) MOE_NORM(1, 1);
-  else if (a.H <= 1024) MOE_NORM(1, 2);
+  else if (a.H <= 1024 && !few) MOE_NORM(1, 2);
   else if (a.H <= 2048) MOE_NORM(4, 1);
-  else if (a.H <= 4096) MOE_NORM(4, 2);
-  else if (a.H <= 8192) MOE_NORM(16, 1);
+  else if (a.H <= 4096 && !few) MOE_NORM(4, 2);
+  else if (a.H <= 8192 && few) MOE_NORM(16, 1);
+  else if (a.H <= 8192) MOE_NORM(8, 2);
   else if (a.H <= 16384) MOE_NORM(16, 2);
   else
     hipLaunchKernelGGL(norm_long_kernel<BF16>, dim3((unsigned)std::min((long long)a.rows, 2LL * cu_count())), dim3(1024), 0, s,
@@ -458,8 +507,7 @@ int norm_grad_any(const NormArgs& a, hipStream_t s) {
   const int parts = norm_parts(a.rows, a.H);  // (none without rows: the sums over them are zeros)
   auto go = [&](auto wpr, auto ch) {
     constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
-    const size_t lds = WPR < 16 ? (size_t)a.H * 8 : 0;
-    hipLaunchKernelGGL((norm_grad_kernel<BF16, WPR, CH>), dim3(parts), dim3(1024), lds, s, a);
+    hipLaunchKernelGGL((norm_grad_kernel<BF16, WPR, CH>), dim3(parts), dim3(1024), 0, s, a);
   };
   using std::integral_constant;
 #define MOE_NORM(W, C) go(integral_constant<int, W>{}, integral_constant<int, C>{})

@@ -34,6 +34,6 @@ inline size_t norm_workspace(int rows, int H) {
 }
 
 int launch_grad_norm(const moe_tensor* t, int n, int clip, float max_norm, float* norm, double* part, hipStream_t s);
-size_t grad_norm_workspace(const moe_tensor* t, int n);
+size_t grad_norm_workspace(int n);
 
 }  // namespace moe

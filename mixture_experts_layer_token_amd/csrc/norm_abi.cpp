@@ -11,7 +11,7 @@ namespace {
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 size_t dt_bytes(int dt) { return dt == MOE_BF16 ? 2 : 4; }
 
-constexpr int kMaxRows = 1 << 24, kMaxH = 1 << 20;
+constexpr int kMaxRows = 1 << 24, kMaxH = 1 << 20, kMaxTensors = 1 << 16;
 
 int check_norm(const moe_norm_desc* d, const char* fn) {
   if (!d) return fail(MOE_ERR_INVALID, "%s: null moe_norm_desc", fn);
@@ -37,16 +37,19 @@ NormArgs norm_args(const moe_norm_desc* d, const void* x, const void* weight) {
 
 // everything about the list; written: whether results are asked for
 int check_tensors(const char* fn, const moe_tensor* t, int n, bool written) {
-  if (n < 0 || n > (1 << 16)) return fail(MOE_ERR_INVALID, "%s: n=%d out of 0..1<<16", fn, n);
+  if (n < 0 || n > kMaxTensors) return fail(MOE_ERR_INVALID, "%s: n=%d out of 0..1<<16", fn, n);
   if (n > 0 && !t) return fail(MOE_ERR_INVALID, "%s: null list", fn);
+  int64_t total = 0;
   for (int i = 0; i < n; ++i) {
     if (!dtype_valid(t[i].dt)) return fail(MOE_ERR_INVALID, "%s: tensor %d: bad dtype %d", fn, i, t[i].dt);
     if (t[i].numel < 0 || t[i].numel > ((int64_t)1 << 40))
       return fail(MOE_ERR_INVALID, "%s: tensor %d: numel=%lld out of 0..1<<40", fn, i, (long long)t[i].numel);
+    total += t[i].numel;
     if (t[i].numel > 0 && !t[i].src) return fail(MOE_ERR_INVALID, "%s: tensor %d: null pointer", fn, i);
     if (!aligned(t[i].src, dt_bytes(t[i].dt)) || !aligned(t[i].dst, dt_bytes(t[i].dt)))
       return fail(MOE_ERR_INVALID, "%s: tensor %d: pointer not aligned to its element type", fn, i);
   }
+  if (total > ((int64_t)1 << 40)) return fail(MOE_ERR_INVALID, "%s: more than 1<<40 elements", fn);
   if (!written) return MOE_OK;
   // A result may be its own gradient in place; anything else that overlaps it (the same gradient named twice among them) would
   // be read or scaled twice in an order that nothing fixes.
@@ -85,7 +88,7 @@ int grad_norm_call(const char* fn, const moe_tensor* t, int n, bool clip, float 
   if (rc != MOE_OK) return rc;
   if (clip && (!(max_norm > 0.f) || !std::isfinite(max_norm))) return fail(MOE_ERR_INVALID, "%s: max_norm=%g", fn, (double)max_norm);
   if (!norm || !aligned(norm, 4)) return fail(MOE_ERR_INVALID, "%s: null or misaligned norm", fn);
-  const size_t need = grad_norm_workspace(t, n);
+  const size_t need = grad_norm_workspace(n);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes (need %zu, 256-byte aligned)", fn, ws ? ws_bytes : 0, need);
   return launch_grad_norm(t, n, clip, max_norm, norm, (double*)ws, (hipStream_t)stream);
@@ -138,14 +141,7 @@ extern "C" int moe_norm_grad(const moe_norm_desc* d, const void* dy, const void*
   return launch_norm_grad(a, d->dt, (hipStream_t)stream);
 }
 
-extern "C" size_t moe_grad_norm_workspace(const moe_tensor* t, int n) {
-  try {
-    if (check_tensors("moe_grad_norm_workspace", t, n, false) != MOE_OK) return 0;
-  } catch (...) {
-    return 0;
-  }
-  return grad_norm_workspace(t, n);
-}
+extern "C" size_t moe_grad_norm_workspace(int n) { return n < 0 || n > kMaxTensors ? 0 : grad_norm_workspace(n); }
 
 extern "C" int moe_grad_norm(const moe_tensor* t, int n, float* norm, void* ws, size_t ws_bytes, void* stream) {
   return grad_norm_call("moe_grad_norm", t, n, false, 0.f, norm, ws, ws_bytes, stream);

@@ -122,13 +122,13 @@ def only_norm(t, n=None, norm_out=P, ws=P, nws=1 << 20):
 A, B, C = 1 << 20, 1 << 21, 1 << 22  # addresses
 
 
-@pytest.mark.parametrize("bad", [(A, A, -1, F32), (A, A, (1 << 40) + 1, F32), (A, A, 4, 2), (None, None, 4, F32), (A + 2, A + 2, 4, F32),
+@pytest.mark.parametrize("bad", [(A, A, -1, F32), (A, A, 4, 2), (None, None, 4, F32), (A + 2, A + 2, 4, F32),
                                  (A + 1, None, 4, BF16), (A, B + 1, 4, BF16)])
 def test_clip_entries(bad):
     good = (C, C, 16, F32)
     for t in (entries(bad), entries(good, bad)):
         assert clip(t) == INVALID and only_norm(t) == INVALID
-        assert L.moe_grad_norm_workspace(t, len(t)) == 0
+        assert b"tensor %d" % (len(t) - 1) in L.moe_last_error()
 
 
 @pytest.mark.parametrize("spans", [
@@ -156,13 +156,18 @@ def test_clip_arguments():
     for n in (-1, (1 << 16) + 1):
         assert clip(t, n=n) == INVALID and only_norm(t, n=n) == INVALID
     assert L.moe_clip_grad_norm(None, 1, 1.0, P, P, 1 << 20, None) == INVALID
-    need = L.moe_grad_norm_workspace(t, 1)
+    need = L.moe_grad_norm_workspace(1)
     assert need > 0
     for ws, n in ((None, need), (P, need - 1), (ctypes.c_void_p(4096 + 8), need)):
         assert clip(t, ws=ws, nws=n) == WORKSPACE and only_norm(t, ws=ws, nws=n) == WORKSPACE
 
 
 def test_workspace_grows_with_the_list():
-    small = L.moe_grad_norm_workspace(entries((A, A, 1, F32)), 1)
-    many = entries(*[(A + (i << 24), A + (i << 24), 1 << 20, BF16) for i in range(400)])
-    assert small < L.moe_grad_norm_workspace(many, 400) <= 1 << 20
+    sizes = [L.moe_grad_norm_workspace(n) for n in (0, 1, 400, 1 << 16)]
+    assert sizes == sorted(sizes) and sizes[0] > 0 and sizes[3] > sizes[1] and all(n % 256 == 0 for n in sizes)
+    assert L.moe_grad_norm_workspace(-1) == 0 and L.moe_grad_norm_workspace((1 << 16) + 1) == 0
+
+
+def test_too_many_elements():
+    t = entries((A, None, 1 << 39, F32), (A, None, 1 << 39, F32), (A, None, 1, F32))
+    assert clip(t) == INVALID and only_norm(t) == INVALID

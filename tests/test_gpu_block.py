@@ -344,6 +344,29 @@ def test_expert_strides_and_another_stream():
     assert torch.equal(a, b) and torch.equal(p, q)
 
 
+def test_rows_of_results_and_operands_far_apart():
+    """Offsets past 32 bits: rows of h, and of dy, 2^24 elements apart (more than 4 GiB in all)."""
+    dt = torch.bfloat16
+    rows, I, K, ld = 140, 64, 64, 1 << 24
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(10)
+    x = torch.randn((rows, K), generator=gen, device="cuda").to(dt)
+    w = (torch.randn((1, 2 * I, K), generator=gen, device="cuda") * 0.2).to(dt)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    near, far = torch.empty((rows, I), device="cuda", dtype=dt), torch.empty((rows, ld), device="cuda", dtype=dt)
+    moe.moe_grouped_swiglu(x, w, off, near)
+    moe.moe_grouped_swiglu(x, w, off, far[:, :I])
+    torch.cuda.synchronize()
+    assert torch.equal(near, far[:, :I])
+    far[:, :K] = x
+    down, gu = w[:, :K, :I].contiguous(), torch.randn((rows, 2 * I), generator=gen, device="cuda").to(dt)
+    a, b = torch.empty_like(gu), torch.empty_like(gu)
+    moe.moe_grouped_swiglu_dx(x, down, gu, off, a)
+    moe.moe_grouped_swiglu_dx(far[:, :K], down, gu, off, b)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 def test_refusals_of_the_python_names():
     dt = torch.bfloat16
     x, w, off = (torch.zeros(s, device="cuda", dtype=dt) for s in ((4, 32), (2, 128, 32), (3,)))
