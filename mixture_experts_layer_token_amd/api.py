@@ -214,7 +214,7 @@ def _ptr(t):
 
 def _rowp(t):
     """Address of a device tensor whose last dimension is contiguous (rows may be strided)."""
-    assert t.is_cuda and (t.shape[-1] <= 1 or t.stride(-1) == 1), "expected a device tensor with contiguous rows"
+    assert t.is_cuda and (t.shape[-1] <= 1 or t.stride(-1) == 1 or t.numel() == 0), "expected a device tensor with contiguous rows"
     return t.data_ptr()
 
 
