@@ -21,6 +21,7 @@ MODE = {"auto": 0, "decode": 1, "prefill": 2, "decode_mx": 3}
 ACT = {"none": 0, "swiglu": 1}
 POLICY = {"lru": 0, "lfu_decay": 1}
 TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+_DT_OF = {torch.float32: DT["f32"], torch.bfloat16: DT["bf16"]}
 
 
 def _dp(t):
@@ -252,6 +253,29 @@ def _launch(f, args, tensors, stream):
             check(f(*args, s))
 
 
+def _run(f, args, dev, stream):
+    """_launch for tensors that are known to be on device `dev`."""
+    if dev < 0:
+        raise ValueError("device tensors expected")
+    _check_stream(stream, dev)
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        check(f(*args, s))
+    else:
+        with torch.cuda.device(dev):
+            check(f(*args, s))
+
+
+def _flat(t, dtype, shape, dev, what):
+    """Address of a contiguous tensor of the given type and shape on device `dev` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError("%s: contiguous %s %s on device %d expected, got %s %s, strides %s, on device %d" % (
+            what, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.stride(), t.get_device()))
+    return t.data_ptr()
+
+
 def _grouped(x, w, y, offsets, perm_src, k) -> MoeGrouped:
     """Descriptor of a grouped product: x [x_rows or rows, K] (dx), w [E, N, K] (dw), y [rows, N] (dy)."""
     E, N, K = w.shape
@@ -312,34 +336,76 @@ def moe_grouped_gemm_dw(dy, x, offsets, dw, perm_src=None, k=1, ws=None, stream=
             (dy, x, dw, offsets, perm_src, ws), stream)
 
 
+def _rows_step(t):
+    """Elements between the rows of a matrix with contiguous rows (0 for one row)."""
+    rows, n = t.shape
+    step, inner = t.stride()
+    if inner != 1 and n > 1 and rows:
+        raise ValueError("contiguous rows expected, got strides (%d, %d)" % (step, inner))
+    if rows <= 1:
+        return 0
+    if step < 1:
+        raise ValueError("a tensor expanded along a dimension has no rows of its own")
+    return step
+
+
+def _block_desc(w, w_rows, rows, offsets, perm_src, k, x_rows, ldx, ldy, dev) -> MoeGrouped:
+    """Descriptor of a gated block: w [E, w_rows * N, K]."""
+    E, N, K = w.shape
+    step_e, ldw, inner = w.stride()
+    if inner != 1 and K > 1:
+        raise ValueError("w: contiguous rows expected, got strides %s" % (w.stride(),))
+    if (E > 1 and step_e < 1) or (N > 1 and ldw < 1):
+        raise ValueError("a tensor expanded along a dimension has no rows of its own")
+    if offsets.dtype is not torch.int32 or offsets.numel() != E + 1 or not offsets.is_contiguous():
+        raise ValueError("offsets: %d int32 entries expected" % (E + 1))
+    src = None
+    if perm_src is not None:
+        if perm_src.dtype is not torch.int32 or perm_src.numel() < rows or not perm_src.is_contiguous():
+            raise ValueError("perm_src: %d int32 entries expected" % rows)
+        if perm_src.get_device() != dev:
+            raise ValueError("perm_src is on another device")
+        src = perm_src.data_ptr()
+    elif x_rows != rows:
+        raise ValueError("x has %d rows, the result %d (pass perm_src to gather)" % (x_rows, rows))
+    if w.get_device() != dev or offsets.get_device() != dev:
+        raise ValueError("tensors on different devices")
+    return MoeGrouped(rows, E, N // w_rows, K, offsets.data_ptr(), src, k, x_rows, ldx, ldy, ldw if N > 1 else 0,
+                      step_e if E > 1 else 0)
+
+
 def moe_grouped_swiglu(x, w, offsets, h, gu=None, perm_src=None, k=1, stream=None):
     """h[p] = SiLU(g) * u with [g | u] = w[e] x[r(p)] for the rows p of every expert e, in one kernel: w [E, 2I, K] (gate
     rows, then up rows) -> h [rows, I]; `gu`: optional [rows, 2I] that takes [g | u] for the backward pass."""
-    if w.dim() != 3 or w.shape[1] % 2:
-        raise ValueError("w: [E, 2I, K] expected, got %s" % (tuple(w.shape),))
-    I = w.shape[1] // 2
-    g, dt = _grouped(x, w[:, :I], h, offsets, perm_src, k), _same_dt(x, w)
-    g.ldw = _step(w, 1)  # (of one gate row alone there is no step)
-    _need(h, x.dtype, (h.shape[0], I), "h")
-    if gu is not None:
-        _need(gu, x.dtype, (h.shape[0], 2 * I), "gu")
-    _launch(lib().moe_grouped_swiglu, (ctypes.byref(g), dt, _rowp(x), _rowp(w), _rowp(h), _ptr(gu)),
-            (x, w, h, gu, offsets, perm_src), stream)
+    if w.dim() != 3 or x.dim() != 2 or h.dim() != 2:
+        raise ValueError("x [.., K], w [E, 2I, K] and h [rows, I] expected")
+    dt, dev = x.dtype, x.get_device()
+    rows, I = h.shape
+    x_rows, K = x.shape
+    if w.shape[1] != 2 * I or w.shape[2] != K:
+        raise ValueError("gated block: x %s, w %s, h %s" % (tuple(x.shape), tuple(w.shape), tuple(h.shape)))
+    if w.dtype is not dt or h.dtype is not dt:
+        raise TypeError("operands must have one type, got %s, %s and %s" % (dt, w.dtype, h.dtype))
+    if h.get_device() != dev:
+        raise ValueError("tensors on different devices")
+    g = _block_desc(w, 2, rows, offsets, perm_src, k, x_rows, _rows_step(x), _rows_step(h), dev)
+    _run(lib().moe_grouped_swiglu, (ctypes.byref(g), _dt(x), x.data_ptr(), w.data_ptr(), h.data_ptr(),
+                                    _flat(gu, dt, (rows, 2 * I), dev, "gu")), dev, stream)
 
 
 def moe_grouped_swiglu_dx(dy, w, gu, offsets, dgu, h=None, stream=None):
     """The gradient of [g | u] from that of the rows behind the down matrices w [E, H, I], in one kernel: dgu [rows, 2I] from
     dy [rows, H] and gu [rows, 2I]; `h`: optional [rows, I] that takes SiLU(g) * u again."""
-    if w.dim() != 3:
-        raise ValueError("w: [E, H, I] expected, got %s" % (tuple(w.shape),))
+    if w.dim() != 3 or dy.dim() != 2 or dy.shape[1] != w.shape[1]:
+        raise ValueError("gated block: dy %s, w %s: [rows, H] and [E, H, I] expected" % (tuple(dy.shape), tuple(w.shape)))
+    dt, dev = dy.dtype, dy.get_device()
     rows, I = dy.shape[0], w.shape[2]
-    _need(dgu, dy.dtype, (rows, 2 * I), "dgu")
-    _need(gu, dy.dtype, (rows, 2 * I), "gu")
-    if h is not None:
-        _need(h, dy.dtype, (rows, I), "h")
-    g, dt = _grouped(dgu[:, :I], w, dy, offsets, None, 1), _same_dt(dy, w)
-    _launch(lib().moe_grouped_swiglu_dx,
-            (ctypes.byref(g), dt, _rowp(dy), _rowp(w), _ptr(gu), _ptr(dgu), _ptr(h)), (dy, w, gu, dgu, h, offsets), stream)
+    if w.dtype is not dt:
+        raise TypeError("operands must have one type, got %s and %s" % (dt, w.dtype))
+    g = _block_desc(w, 1, rows, offsets, None, 1, rows, 0, _rows_step(dy), dev)
+    _run(lib().moe_grouped_swiglu_dx,
+         (ctypes.byref(g), _dt(dy), dy.data_ptr(), w.data_ptr(), _flat(gu, dt, (rows, 2 * I), dev, "gu"),
+          _flat(dgu, dt, (rows, 2 * I), dev, "dgu"), _flat(h, dt, (rows, I), dev, "h")), dev, stream)
 
 
 def _need(t, dtype, shape, what):
@@ -395,26 +461,37 @@ def moe_swiglu_grad(gu, dh, dgu, h=None, n_rows=None, stream=None):
             (gu, dh, dgu, h, n_rows), stream)
 
 
-def _norm_desc(x, y, params, eps, rms) -> MoeNormDesc:
-    """Descriptor of a norm of rows; params: weight, bias and their gradients, None where there are none."""
-    if x.dim() != 2 or y.shape != x.shape:
-        raise ValueError("norm: x %s, y %s" % (tuple(x.shape), tuple(y.shape)))
-    rows, H = x.shape
-    params = [t for t in params if t is not None]
+def _norm_call(x, y, params, eps, rms, dev):
+    """Descriptor of a norm of rows, and the addresses of params: weight, bias and their gradients (None -> NULL)."""
+    shape = x.shape
+    if len(shape) != 2 or y.shape != shape:
+        raise ValueError("norm: x %s, y %s" % (tuple(shape), tuple(y.shape)))
+    if y.dtype is not x.dtype:
+        raise TypeError("operands must have one type, got %s and %s" % (x.dtype, y.dtype))
+    if y.get_device() != dev:
+        raise ValueError("tensors on different devices")
+    rows, H = shape
+    pdt, at = None, []
     for t in params:
-        _need(t, params[0].dtype, (H,), "weight, bias and their gradients")
-    pdt = _dt(params[0]) if params else DT["f32"]
-    return MoeNormDesc(rows, H, int(rms), _same_dt(x, y), pdt, eps, _step(x, 0), _step(y, 0))
+        if t is None:
+            at.append(None)
+            continue
+        if pdt is None:
+            pdt = t.dtype
+        at.append(_flat(t, pdt, (H,), dev, "weight, bias and their gradients"))
+    types = _DT_OF.get(x.dtype), 0 if pdt is None else _DT_OF.get(pdt)
+    if None in types:
+        raise TypeError("rows and parameters must be float32 or bfloat16, got %s and %s" % (x.dtype, pdt))
+    return MoeNormDesc(rows, H, int(rms), types[0], types[1], eps, _rows_step(x), _rows_step(y)), at
 
 
 def moe_norm(x, weight, bias, y, eps=1e-5, rms=False, stats=None, stream=None):
     """y = layer norm of the rows of x [rows, H] (RMS norm with rms=True), times `weight` [H] and plus `bias` [H] (None: without);
     `stats`: optional float32 [rows, 2] that takes every row's mean and 1 / sqrt(variance + eps) for the backward pass."""
-    d = _norm_desc(x, y, (weight, bias), eps, rms)
-    if stats is not None:
-        _need(stats, torch.float32, (d.rows, 2), "stats")
-    _launch(lib().moe_norm, (ctypes.byref(d), _rowp(x), _ptr(weight), _ptr(bias), _rowp(y), _ptr(stats)),
-            (x, weight, bias, y, stats), stream)
+    dev = x.get_device()
+    d, (w, b) = _norm_call(x, y, (weight, bias), eps, rms, dev)
+    _run(lib().moe_norm, (ctypes.byref(d), x.data_ptr(), w, b, y.data_ptr(),
+                          _flat(stats, torch.float32, (d.rows, 2), dev, "stats")), dev, stream)
 
 
 def moe_norm_workspace(rows, H) -> int:
@@ -424,15 +501,17 @@ def moe_norm_workspace(rows, H) -> int:
 def moe_norm_grad(dy, x, weight, stats, dx, dweight=None, dbias=None, add=None, rms=False, ws=None, stream=None):
     """Gradients of moe_norm: dx [rows, H] (plus `add`, a gradient that reaches x on another way), dweight and dbias [H] where
     given.  `ws`: device workspace of at least moe_norm_workspace bytes (allocated here if None)."""
-    d = _norm_desc(x, dy, (weight, dweight, dbias), 0.0, rms)
-    _need(stats, torch.float32, (d.rows, 2), "stats")
-    _need(dx, x.dtype, x.shape, "dx")
-    if add is not None:
-        _need(add, x.dtype, x.shape, "add")
+    dev = x.get_device()
+    d, (w, dw, db) = _norm_call(x, dy, (weight, dweight, dbias), 0.0, rms, dev)
+    dt, shape = x.dtype, x.shape
+    if stats is None or dx is None:
+        raise ValueError("stats and dx expected")
+    at = (dy.data_ptr(), x.data_ptr(), w, _flat(stats, torch.float32, (d.rows, 2), dev, "stats"),
+          _flat(add, dt, shape, dev, "add"), _flat(dx, dt, shape, dev, "dx"), dw, db)
     ws, wp, wn = _own_ws(ws, lambda: moe_norm_workspace(d.rows, d.H), x.device, stream)
-    _launch(lib().moe_norm_grad,
-            (ctypes.byref(d), _rowp(dy), _rowp(x), _ptr(weight), _ptr(stats), _ptr(add), _ptr(dx), _ptr(dweight), _ptr(dbias),
-             wp, wn), (x, dy, weight, stats, add, dx, dweight, dbias, ws), stream)
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError("the workspace is on another device")
+    _run(lib().moe_norm_grad, (ctypes.byref(d), *at, wp, wn), dev, stream)
 
 
 def _own_ws(ws, need, device, stream):
@@ -460,19 +539,18 @@ def _is_dense(t):
     return True
 
 
-_DT_OF = {torch.float32: DT["f32"], torch.bfloat16: DT["bf16"]}
-
-
 def _tensor_list(grads, outs):
-    """moe_tensor entries of a list of gradients and of where their results go (four 64-bit words each), and their device.  Column
-    by column: a list of hundreds of tensors costs more time here than on the GPU."""
+    """moe_tensor entries of a list of gradients and of where their results go (four 64-bit words each), and their devices.
+    Column by column: a list of hundreds of tensors costs more time here than on the GPU."""
     devices = {g.get_device() for g in grads}
     numel = [g.numel() for g in grads]
+    dtypes = [g.dtype for g in grads]
     try:
-        types = [_DT_OF[g.dtype] for g in grads]
+        types = [_DT_OF[d] for d in dtypes]
     except KeyError as e:
         raise TypeError("gradients must be float32 or bfloat16, got %s" % e.args[0])
-    if not all([g.is_contiguous() for g in grads]) and not all(map(_is_dense, grads)):
+    whole = all([g.is_contiguous() for g in grads])
+    if not whole and not all(map(_is_dense, grads)):
         raise ValueError("gradients without gaps expected")
     src = [g.data_ptr() for g in grads]
     if outs is None:
@@ -480,21 +558,23 @@ def _tensor_list(grads, outs):
     elif outs is grads:
         dst = src
     else:
-        dst = [0 if o is None else o.data_ptr() for o in outs]
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if o is None:
-                continue
-            if o.dtype is not g.dtype or o.shape != g.shape or not (
-                    o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride()):
-                raise ValueError("result %d does not have its gradient's type, shape and strides" % i)
-            if o.get_device() not in devices:
-                raise ValueError("result %d is on another device" % i)
+        if type(None) not in map(type, outs):
+            same = whole and all([o.is_contiguous() for o in outs]) and [o.numel() for o in outs] == numel \
+                and [o.dtype for o in outs] == dtypes
+            dst = [o.data_ptr() for o in outs]
+        else:
+            same, dst = False, [0 if o is None else o.data_ptr() for o in outs]
+        if not same:
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                if o is not None and (o.dtype is not g.dtype or o.shape != g.shape or not (
+                        o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride())):
+                    raise ValueError("result %d does not have its gradient's type, size and strides" % i)
+        devices |= {o.get_device() for o in outs if o is not None}
     if len(devices) > 1 or -1 in devices:
-        raise ValueError("gradients on one GPU expected")
-    words = array.array("q", bytes(32 * len(src)))
-    words[0::4], words[1::4] = array.array("q", src), array.array("q", dst)
-    words[2::4], words[3::4] = array.array("q", numel), array.array("q", types)
-    return words, devices
+        raise ValueError("gradients and results on one GPU expected")
+    words = [0] * (4 * len(src))
+    words[0::4], words[1::4], words[2::4], words[3::4] = src, dst, numel, types
+    return array.array("q", words), devices
 
 
 def _grad_norm(f, grads, outs, args, norm, ws, stream):
@@ -504,7 +584,9 @@ def _grad_norm(f, grads, outs, args, norm, ws, stream):
         raise ValueError("norm on device %d, gradients on another" % norm.get_device())
     n = len(grads)
     ws, wp, wn = _own_ws(ws, lambda: moe_grad_norm_workspace(n), norm.device, stream)
-    _launch(f, (words.buffer_info()[0], n, *args, _ptr(norm), wp, wn), (norm, ws), stream)
+    if ws is not None and ws.get_device() != norm.get_device():
+        raise ValueError("the workspace is on another device")
+    _run(f, (words.buffer_info()[0], n, *args, _ptr(norm), wp, wn), norm.get_device(), stream)
 
 
 def moe_grad_norm_workspace(n) -> int:

@@ -65,20 +65,25 @@ __device__ __forceinline__ float element(gptr p, int i) {
   if constexpr (BF16) return bf16_to_f32(((const __attribute__((address_space(1))) unsigned short*)p)[i]);
   return ((const __attribute__((address_space(1))) float*)p)[i];
 }
-template <bool BF16>
+// PAST: without keeping the lines in the caches
+template <bool BF16, bool PAST>
 __device__ __forceinline__ void store_eight(char* p, int i, const float (&v)[8]) {
   typedef u32x4 __attribute__((aligned(1))) any4;
   typedef __attribute__((address_space(1))) any4* anyp;
   typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 b2;
   const anyp o = (anyp)((__attribute__((address_space(1))) char*)p + (size_t)i * (BF16 ? 2 : 4));
+  auto put = [&](anyp to, u32x4 w) {
+    if constexpr (PAST) __builtin_nontemporal_store((any4)w, to);
+    else *to = w;
+  };
   if constexpr (BF16) {
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(unsigned, b2{(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
-    *o = w;
+    put(o, w);
   } else {
-    o[0] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
-    o[1] = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+    put(o, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+    put(o + 1, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
   }
 }
 // f(i, eight) for the thread's groups of 8 elements of a chunk, kUnroll passes' loads together, then g(i) for the elements
@@ -139,6 +144,7 @@ __global__ __launch_bounds__(kThreads) void square_sums_kernel(TensorTable tab, 
 }
 
 // parts: of all tables of the call.  A norm that is not finite scales nothing.
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable tab, const double* __restrict__ part, int parts, int clip,
                                                         float max_norm, float* __restrict__ norm) {
   __shared__ double lds[kThreads / 64];
@@ -169,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable tab, const d
         float g[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = x.get(e) * scale * post;
-        store_eight<BF>(o, i, g);
+        store_eight<BF, PAST>(o, i, g);
       }, [&](int i) {
         const float g = element<BF>(p, i) * scale * post;
         if constexpr (BF) ((unsigned short*)o)[i] = f32_to_bf16_rne(g);
@@ -181,19 +187,26 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable tab, const d
   }
 }
 
-// Elements of a chunk: long ones cost less to find, short ones fill the card when there is little to do.
-int chunk_elements(const moe_tensor* t, int n) {
-  long long total = 0;
-  for (int i = 0; i < n; ++i) total += t[i].numel;
+// What the size of the call decides.
+struct Plan {
+  int chunk;  // elements: long chunks cost less to find, short ones fill the card when there is little to do
+  // Results past the caches where the gradients are more than a quarter of the last-level cache: the results would drive out
+  // gradients that are still to be read (193 tensors of 345 MB in all 240 -> 204 us), while smaller ones stay for the optimizer.
+  bool past;
+};
+Plan plan_of(const moe_tensor* t, int n) {
+  long long total = 0, bytes = 0;
+  for (int i = 0; i < n; ++i) total += t[i].numel, bytes += t[i].numel * (t[i].dt == MOE_BF16 ? 2 : 4);
   int chunk = kStep;
   while (chunk < kMaxChunk && total / chunk > 4 * kBlocks) chunk *= 2;
-  return chunk;
+  return Plan{chunk, bytes > (64 << 20)};
 }
 
 // Tables of the call: as few as hold it, of about equal length.
 int tables_of(int n) { return (n + kTensors - 1) / kTensors; }
 // the next table of tensors from `at` on (empty ones left out); at moves past them
-void next_table(const moe_tensor* t, int n, int chunk, int& at, TensorTable& tab) {
+void next_table(const moe_tensor* t, int n, const Plan& p, int& at, TensorTable& tab) {
+  const int chunk = p.chunk;
   tab.n = tab.chunks = 0, tab.chunk = chunk;
   const int each = (n + std::max(tables_of(n), 1) - 1) / std::max(tables_of(n), 1);
   for (const int end = std::min(n, at + each); at < end; ++at) {
@@ -214,11 +227,11 @@ size_t grad_norm_workspace(int n) { return ((size_t)std::max(tables_of(n), 1) * 
 
 int launch_grad_norm(const moe_tensor* t, int n, int clip, float max_norm, float* norm, double* part, hipStream_t s) {
   int parts = 0;
-  const int chunk = chunk_elements(t, n);
+  const Plan plan = plan_of(t, n);
   TensorTable tab;
   tab.n = tab.chunks = 0;
   for (int at = 0; at < n;) {
-    next_table(t, n, chunk, at, tab);
+    next_table(t, n, plan, at, tab);
     if (!tab.n) continue;
     hipLaunchKernelGGL(square_sums_kernel, dim3(blocks_of(tab)), dim3(kThreads), 0, s, tab, part + parts);
     parts += blocks_of(tab);
@@ -228,10 +241,12 @@ int launch_grad_norm(const moe_tensor* t, int n, int clip, float max_norm, float
   const int tables = std::max(tables_of(n), 1), each = (n + tables - 1) / tables;
   for (int i = tables - 1; i >= 0; --i) {
     int at = i * each;
-    if (tables > 1) next_table(t, n, chunk, at, tab);
+    if (tables > 1) next_table(t, n, plan, at, tab);
     if (i < tables - 1 && (!clip || !tab.n)) continue;
-    hipLaunchKernelGGL(clip_kernel, dim3(clip ? std::max(blocks_of(tab), 1) : 1), dim3(kThreads), 0, s, tab, part, parts, clip,
-                       max_norm, i == tables - 1 ? norm : nullptr);
+    const dim3 grid(clip ? std::max(blocks_of(tab), 1) : 1);
+    float* to = i == tables - 1 ? norm : nullptr;
+    if (plan.past) hipLaunchKernelGGL(clip_kernel<true>, grid, dim3(kThreads), 0, s, tab, part, parts, clip, max_norm, to);
+    else hipLaunchKernelGGL(clip_kernel<false>, grid, dim3(kThreads), 0, s, tab, part, parts, clip, max_norm, to);
   }
   MOE_CHECK_LAUNCH("moe_clip_grad_norm launch");
   return MOE_OK;

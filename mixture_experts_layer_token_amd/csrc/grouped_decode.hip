@@ -55,22 +55,29 @@ struct Rows {
   }
 };
 
-// GLU: the gated block.  Gate and up rows of the same 16 features, so half as many bytes of weights per feature's worth of x;
-// the sums of the gate's strip pass through LDS first, then those of the up strip, and the same thread holds both.
-template <int TYPE, bool DIRECT, int MT, bool GLU>
+// GLU: the gated block.  kStrips: a strip of 16 gate rows and one of 16 up rows to a workgroup, so that the rows of x are read
+// once for both; the sums of the gate's strip pass through LDS first, then those of the up strip.  kHalves: one strip of 8 gate
+// rows and 8 up rows, for twice as many workgroups where there are few.
+enum GluForm { kNoGlu, kStrips, kHalves };
+template <int TYPE, bool DIRECT, int MT, int GLU>
 __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, int rows, int n0, char* smem) {
   typedef TileT<TYPE> TT;
   typedef typename TT::Frag Frag;
   typedef typename TT::Acc Acc;
-  constexpr int EB = TT::EB, D = MT == 1 ? 4 : MT == 2 ? 3 : 2, S = GLU ? 2 : 1;  // S: strips of 16 weight rows
+  constexpr int EB = TT::EB, D = MT == 1 ? 4 : MT == 2 ? 3 : 2, S = GLU == kStrips ? 2 : 1;  // S: strips of 16 weight rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  const int len = a.K * EB, nj = min(kDecodeCols, a.N - n0);
+  const int len = a.K * EB, nj = min(GLU == kHalves ? kDecodeCols / 2 : kDecodeCols, a.N - n0);
   Rows<EB, DIRECT> W[S], X[MT];
   const gptr w = (gptr)a.w + ((size_t)e * a.w_stride + (size_t)n0 * a.ldw) * EB;
+  if constexpr (GLU == kHalves) {
+    const long long r = min(lane & 7, nj - 1) + (lane & 8 ? a.N : 0);
+    W[0].init(w, (unsigned)((a.N + nj - 1) * a.ldw * EB) + len, r * a.ldw * EB, len);
+  } else {
 #pragma unroll
-  for (int z = 0; z < S; ++z)
-    W[z].init(w + (z ? (size_t)a.N * a.ldw * EB : 0), (unsigned)((nj - 1) * a.ldw * EB) + len,
-              (long long)min(lane & 15, nj - 1) * a.ldw * EB, len);
+    for (int z = 0; z < S; ++z)
+      W[z].init(w + (z ? (size_t)a.N * a.ldw * EB : 0), (unsigned)((nj - 1) * a.ldw * EB) + len,
+                (long long)min(lane & 15, nj - 1) * a.ldw * EB, len);
+  }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = p0 + min(16 * m + (lane & 15), rows - 1);
@@ -125,18 +132,21 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
 #pragma unroll
   for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[0][m];
   __syncthreads();
-  if constexpr (GLU) {
+  if constexpr (GLU != kNoGlu) {
     const int t = threadIdx.x, m = t >> 6, i = 16 * m + (t & 15), jj = ((t & 63) >> 4) * 4;
-    const bool mine = t < MT * 64 && i < rows;  // (MT * 64 <= blockDim.x)
+    // (MT * 64 <= blockDim.x.  Halves: rows 0..7 of the strip, in lanes 0..31, are the gate's, their up rows 32 lanes on)
+    const bool mine = t < MT * 64 && i < rows && (GLU == kStrips || (t & 32) == 0);
     Acc g = Acc{}, u = Acc{};
     if (mine)
       for (int o = 0; o < nw; ++o) g += part[o * MT * 64 + t];
-    __syncthreads();
+    if constexpr (GLU == kStrips) {
+      __syncthreads();
 #pragma unroll
-    for (int q = 0; q < MT; ++q) part[(wave * MT + q) * 64 + lane] = acc[S - 1][q];
-    __syncthreads();
+      for (int q = 0; q < MT; ++q) part[(wave * MT + q) * 64 + lane] = acc[S - 1][q];
+      __syncthreads();
+    }
     if (!mine) return;
-    for (int o = 0; o < nw; ++o) u += part[o * MT * 64 + t];
+    for (int o = 0; o < nw; ++o) u += part[o * MT * 64 + t + (GLU == kHalves ? 32 : 0)];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (jj + r >= nj) break;
@@ -170,10 +180,11 @@ __device__ __forceinline__ void decode_body(const GroupArgs& a, int e, int p0, i
   }
 }
 
-template <int TYPE, bool DIRECT, bool GLU>
-__global__ __launch_bounds__(512) void grouped_decode_kernel(GroupArgs a) {
-  __shared__ __align__(16) char smem[8 * 4 * 64 * 16];
-  const int ncol = (a.N + kDecodeCols - 1) / kDecodeCols;
+template <int TYPE, bool DIRECT, int GLU>
+__global__ __launch_bounds__(GLU ? 256 : 512) void grouped_decode_kernel(GroupArgs a) {
+  __shared__ __align__(16) char smem[(GLU ? 4 : 8) * 4 * 64 * 16];
+  constexpr int COLS = GLU == kHalves ? kDecodeCols / 2 : kDecodeCols;
+  const int ncol = (a.N + COLS - 1) / COLS;
   const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, kDecodeRows, ncol, 0, 1);
   if ((int)blockIdx.x >= sc.total) return;
   const GroupSpan g = sc.find(a.offsets, a.E, a.rows, blockIdx.x);
@@ -181,16 +192,18 @@ __global__ __launch_bounds__(512) void grouped_decode_kernel(GroupArgs a) {
   const int r0 = tile * kDecodeRows, rows = min(kDecodeRows, g.n - r0), mt = (rows + 15) / 16;
   static_for<kDecodeRows / 16>([&](auto mc) {
     constexpr int MT = mc + 1;
-    if (mt == MT) decode_body<TYPE, DIRECT, MT, GLU>(a, g.e, g.p0 + r0, rows, col * kDecodeCols, smem);
+    if (mt == MT) decode_body<TYPE, DIRECT, MT, GLU>(a, g.e, g.p0 + r0, rows, col * COLS, smem);
   });
 }
 
-template <int TYPE, bool GLU = false>
+template <int TYPE, int GLU = kNoGlu>
 int decode_launch(const GroupArgs& a, bool direct, hipStream_t s) {
-  const long long nb = group_tiles_max(a.rows, a.E, kDecodeRows) * ((a.N + kDecodeCols - 1) / kDecodeCols);
+  constexpr int COLS = GLU == kHalves ? kDecodeCols / 2 : kDecodeCols;
+  const long long nb = group_tiles_max(a.rows, a.E, kDecodeRows) * ((a.N + COLS - 1) / COLS);
   if (nb == 0) return MOE_OK;
-  // 8 waves where there are few workgroups: each then has half the groups to walk
-  const int threads = nb < 1024 ? 512 : 256;
+  // 8 waves where there are few workgroups: each then has half the groups to walk.  (The gated block has twice the loads per
+  // workgroup, and 4 waves are enough: one row to 4 experts of 5760 x 2880 30 us, with 8 waves 38.)
+  const int threads = GLU || nb >= 1024 ? 256 : 512;
   if (nb > kMaxThreads / threads) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_gemm: %lld tiles in one launch", nb);
   if (direct)
     hipLaunchKernelGGL((grouped_decode_kernel<TYPE, true, GLU>), dim3((unsigned)nb), dim3(threads), 0, s, a);
@@ -200,6 +213,15 @@ int decode_launch(const GroupArgs& a, bool direct, hipStream_t s) {
   return MOE_OK;
 }
 
+// Halves while strips would leave half of the compute units idle.  Measured, halves against strips (us, weights not in a cache):
+// 32 workgroups of strips (512 x 7168, 1 row) 13.5 : 18.9, 90 (1440 x 2880) 9.2 : 11.3, 128 (2048 x 7168) 13.8 : 19.1, 180 (1440 x 2880,
+// 2 experts) 12.2 : 11.3, 256 (4096 x 4096) 15.8 : 16.7 and (2048 x 7168, 2 experts) 27.0 : 25.4, 720 (2880 x 2880, 4 experts) 33.5 : 30.6.
+template <int TYPE>
+int glu_launch(const GroupArgs& a, bool direct, hipStream_t s) {
+  const long long strips = group_tiles_max(a.rows, a.E, kDecodeRows) * ((a.N + kDecodeCols - 1) / kDecodeCols);
+  return 2 * strips <= cu_count() ? decode_launch<TYPE, kHalves>(a, direct, s) : decode_launch<TYPE, kStrips>(a, direct, s);
+}
+
 }  // namespace
 
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s) {
@@ -207,7 +229,7 @@ int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t
                      : type == kF32 ? decode_launch<kF32>(a, direct, s) : decode_launch<kBf16>(a, direct, s);
 }
 int launch_glu_decode(const GroupArgs& a, int type, bool direct, hipStream_t s) {
-  return type == kF32 ? decode_launch<kF32, true>(a, direct, s) : decode_launch<kBf16, true>(a, direct, s);
+  return type == kF32 ? glu_launch<kF32>(a, direct, s) : glu_launch<kBf16>(a, direct, s);
 }
 
 }  // namespace moe
