@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 
 import numpy as np
 import torch
@@ -539,37 +540,42 @@ def _is_dense(t):
     return True
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _tensor_list(grads, outs):
     """moe_tensor entries of a list of gradients and of where their results go (four 64-bit words each), and their devices.
-    Column by column: a list of hundreds of tensors costs more time here than on the GPU."""
-    devices = {g.get_device() for g in grads}
-    numel = [g.numel() for g in grads]
-    dtypes = [g.dtype for g in grads]
+    Column by column and without a Python function per tensor: hundreds of tensors cost more time here than on the GPU."""
+    T = torch.Tensor
+    devices = set(map(T.get_device, grads))
+    numel = list(map(T.numel, grads))
+    dtypes = list(map(_dtype_of, grads))
     try:
-        types = [_DT_OF[d] for d in dtypes]
+        types = list(map(_DT_OF.__getitem__, dtypes))
     except KeyError as e:
         raise TypeError("gradients must be float32 or bfloat16, got %s" % e.args[0])
-    whole = all([g.is_contiguous() for g in grads])
+    whole = all(map(T.is_contiguous, grads))
     if not whole and not all(map(_is_dense, grads)):
         raise ValueError("gradients without gaps expected")
-    src = [g.data_ptr() for g in grads]
+    src = list(map(T.data_ptr, grads))
     if outs is None:
         dst = [0] * len(src)
     elif outs is grads:
         dst = src
     else:
         if type(None) not in map(type, outs):
-            same = whole and all([o.is_contiguous() for o in outs]) and [o.numel() for o in outs] == numel \
-                and [o.dtype for o in outs] == dtypes
-            dst = [o.data_ptr() for o in outs]
+            same = whole and all(map(T.is_contiguous, outs)) and list(map(T.numel, outs)) == numel \
+                and list(map(_dtype_of, outs)) == dtypes
+            dst = list(map(T.data_ptr, outs))
+            devices.update(map(T.get_device, outs))
         else:
             same, dst = False, [0 if o is None else o.data_ptr() for o in outs]
+            devices.update(o.get_device() for o in outs if o is not None)
         if not same:
             for i, (g, o) in enumerate(zip(grads, outs)):
                 if o is not None and (o.dtype is not g.dtype or o.shape != g.shape or not (
                         o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride())):
                     raise ValueError("result %d does not have its gradient's type, size and strides" % i)
-        devices |= {o.get_device() for o in outs if o is not None}
     if len(devices) > 1 or -1 in devices:
         raise ValueError("gradients and results on one GPU expected")
     words = [0] * (4 * len(src))

@@ -60,6 +60,10 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
 //          1 row 71 : 83, 8 rows 91 : 84;  4095 x 4097, 8 experts (256): 1 row 159 : 119, 32 rows 386 : 124
 //   fp32 (bound by the matrix cores, of which its many workgroups use more at a time)   4096 x 14336, 8 experts (256):
 //          8 rows 387 : 466, 16 rows 490 : 466;  14336 x 4096, 1 expert (112): 48 rows 138 : 145, 64 rows 166 : 146
+// The gated block counts its 2N rows of weights and fits the same rule.  bf16   2 x 2880 x 2880, 1 expert (45): 16 rows 12 : 19, 64 rows
+//          20 : 20;  4 experts of 2 x 1440 x 2880 (92): 8 rows 20 : 20, 32 rows 27 : 21;  8 experts of 2 x 2048 x 4096 (256): 1 row 54 : 65, 16
+//          rows 59 : 65, 32 rows 79 : 65;  64 experts of 2 x 512 x 1024 (512): 1 row 34 : 28;  staged 2 x 1441 x 2881 (23): 48 rows 46 : 68, 64
+//          68 : 67;  fp32   2 x 2880 x 2880 (45): 64 rows 49 : 98;  8 experts of 2 x 2048 x 4096 (256): 16 rows 126 : 149, 32 rows 164 : 150
 bool few_rows_kernel(int type, bool staged, int rows, int N, int E) {
   const long long tiles = (long long)std::min(rows, E) * ((N + 127) / 128), mean = ((long long)rows + E - 1) / E;
   if (mean > kDecodeRows) return false;

@@ -556,21 +556,46 @@ struct TileKernel {
     if constexpr (TYPE == kBf16) return __builtin_amdgcn_rcpf(1.f + __expf(-g));
     return 1.f / (1.f + expf(-g));
   }
-  // 8 neighbouring elements of a row of the operands' type, in memory at any element-aligned address
+  // 8 neighbouring elements of a row of the operands' type, of which the first n exist, in memory at any element-aligned address
   struct Eight {
     u32x4 v[EB / 2];
     __device__ __forceinline__ void load(const char* base, unsigned off) {
 #pragma unroll
       for (int h = 0; h < EB / 2; ++h) v[h] = load_any((gptr)base + off + 16 * h);
     }
+    // n elements from there, one by one
+    __device__ __forceinline__ void load_some(const char* base, unsigned off, int n) {
+#pragma unroll
+      for (int h = 0; h < EB / 2; ++h) v[h] = load_part<EB>((gptr)base + off + 16 * h, n * EB - 16 * h);
+    }
+    // moved down by s elements
+    __device__ __forceinline__ void shift(int s) {
+      if constexpr (EB == 2) {
+        v[0] = shift_bytes(v[0], 2 * s);
+      } else {
+        const int lo = min(s, 4) * 4, hi = max(s - 4, 0) * 4;  // (by up to four, then by the rest)
+        const u32x4 under = shift_bytes(v[0], lo), over = shift_bytes(v[EB / 2 - 1], lo);
+        u32x4 carry = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // the elements of the upper half that come down into the lower one
+#pragma unroll
+          for (int f = 0; f < 4; ++f) carry[e] = e + min(s, 4) - 4 == f ? v[EB / 2 - 1][f] : carry[e];
+        v[0] = shift_bytes(under | carry, hi);
+        v[EB / 2 - 1] = shift_bytes(over, hi);
+      }
+    }
     __device__ __forceinline__ float get(int e) const {
       if constexpr (EB == 2) return __uint_as_float(e % 2 ? v[0][e / 2] & 0xFFFF0000u : v[0][e / 2] << 16);
       return __uint_as_float(v[e / 4 % (EB / 2)][e % 4]);
     }
-    static __device__ __forceinline__ void store(char* base, unsigned off, const float (&f)[8]) {
+    static __device__ __forceinline__ void store(char* base, unsigned off, int n, const float (&f)[8]) {
       typedef u32x4 __attribute__((aligned(1))) any4;
       const auto p = (__attribute__((address_space(1))) char*)base + off;
-      if constexpr (EB == 2) {
+      if (n < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n) store_out(base + off, e, f[e], EB == 2);
+      } else if constexpr (EB == 2) {
         *(__attribute__((address_space(1))) any4*)p =
             u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
       } else {
@@ -579,10 +604,6 @@ struct TileKernel {
       }
     }
   };
-  static __device__ __forceinline__ float load1(const char* p, size_t i) {
-    if constexpr (TYPE == kBf16) return bf16_to_f32(((const unsigned short*)p)[i]);
-    return ((const float*)p)[i];
-  }
 
   // The gate's operands and results cross memory in rows: 16 rows of a wave's accumulators at a time pass through its own LDS
   // region, so that a lane holds 8 neighbouring columns (16 bytes in bf16) and a row's lanes follow one another.  A row of the
@@ -618,12 +639,6 @@ struct TileKernel {
       for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
     }
   }
-  // column c of it
-  static __device__ __forceinline__ float region_one(lptr reg, int row, int c, int up) {
-    const int p = GLU ? c / 16 * 8 + 4 * up + c % 16 / 4 : c / 4;
-    return *(const __attribute__((address_space(3))) float*)(piece(reg, row, p) + c % 4 * 4);
-  }
-
   // Results of the gated block: h = SiLU(g) u from the unrounded sums, and [g | u] itself if it is kept.
   template <int NI>
   static __device__ __forceinline__ void write_glu(const GroupArgs& a, const TileItem& t, const Feed& feed, Acc (&acc)[WJ][NI]) {
@@ -635,40 +650,26 @@ struct TileKernel {
     // the next tile's first stages have landed before the first store: its loop need not wait for stores
     if constexpr (!STAGED) wait_loads<0>();
     const lptr reg = feed.lds + NB * STAGE + wave * REGION;
+    constexpr int RI = 64 / WJ;  // rows at a time: WJ lanes to a row of 8 WJ columns
+    const int m = lane % WJ, col = c0 + 8 * m, n8 = t.nj - col;
 #pragma unroll 1
     for (int i = 0; i < NI; ++i) {
-      const int r0 = 32 * i + wi * 16;
       acc_to_region<NI>(reg, lane, acc, i);
-      if (a.N % 8 == 0) {
-        constexpr int RI = 64 / WJ;  // rows at a time: WJ lanes to a row of 8 WJ columns
-        const int m = lane % WJ, col = c0 + 8 * m;
 #pragma unroll
-        for (int k = 0; k < 16 / RI; ++k) {
-          const int rr = k * RI + lane / WJ, r = r0 + rr;
-          float g[8], u[8], v[8];
-          region_row(reg, rr, m, 0, g);
-          region_row(reg, rr, m, 1, u);
+      for (int k = 0; k < 16 / RI; ++k) {
+        const int rr = k * RI + lane / WJ, r = 32 * i + wi * 16 + rr;
+        float g[8], u[8], v[8];
+        region_row(reg, rr, m, 0, g);
+        region_row(reg, rr, m, 1, u);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = g[e] * sigmoid(g[e]) * u[e];
-          if (r >= t.ni || col >= t.nj) continue;
-          Eight::store(h + (size_t)r * a.ldy * EB, col * EB, v);  // (ldy may be anything; rows of gu end within 32 bits)
-          if (gu) {
-            const unsigned q = (unsigned)(r * (unsigned)ldg + col) * EB;
-            Eight::store(gu, q, g);
-            Eight::store(gu + (size_t)a.N * EB, q, u);
-          }
+        for (int e = 0; e < 8; ++e) v[e] = g[e] * sigmoid(g[e]) * u[e];
+        if (r >= t.ni || n8 <= 0) continue;
+        Eight::store(h + (size_t)r * a.ldy * EB, col * EB, n8, v);  // (ldy may be anything; rows of gu end within 32 bits)
+        if (gu) {
+          const unsigned q = (unsigned)(r * (unsigned)ldg + col) * EB;
+          Eight::store(gu, q, n8, g);
+          Eight::store(gu + (size_t)a.N * EB, q, n8, u);
         }
-      } else {
-#pragma unroll 1
-        for (int r = 0; r < min(t.ni - r0, 16); ++r)
-          if (lane < min(t.nj - c0, 8 * WJ)) {  // (8 WJ <= 64 columns)
-            const float g = region_one(reg, r, lane, 0), u = region_one(reg, r, lane, 1);
-            store_out(h, (size_t)(r0 + r) * a.ldy + c0 + lane, g * sigmoid(g) * u, EB == 2);
-            if (gu) {
-              store_out(gu, (size_t)(r0 + r) * ldg + c0 + lane, g, EB == 2);
-              store_out(gu, (size_t)(r0 + r) * ldg + a.N + c0 + lane, u, EB == 2);
-            }
-          }
       }
     }
   }
@@ -681,20 +682,29 @@ struct TileKernel {
     const int lane = feed.lane, wave = feed.wave, wi = wave >> 1, wj = wave & 1;
     const long long ldg = 2LL * a.K;
     const int c0 = WJ * 16 * wj;
-    const size_t o = ((size_t)t.p0 * ldg + t.j0) * EB, up = (size_t)a.K * EB;
+    const size_t o = (size_t)t.p0 * ldg * EB, up = (size_t)a.K * EB;
     const char* gu = (const char*)a.gu + o;
     char* dgu = (char*)a.dgu + o;
-    char* h = a.h ? (char*)a.h + ((size_t)t.p0 * a.K + t.j0) * EB : nullptr;
+    char* h = a.h ? (char*)a.h + (size_t)t.p0 * a.K * EB : nullptr;
     const lptr reg = feed.lds + NB * STAGE + wave * REGION;
-    if (a.K % 8 == 0) {
-      constexpr int LR = 2 * WJ, RI = 64 / LR, IT = 16 / RI;  // lanes to a row of 16 WJ columns, rows at a time
-      const int m = lane % LR, col = c0 + 8 * m;
-      const unsigned safe = min(col, t.nj - 8);  // (t.nj is a multiple of 8 as well)
+    constexpr int LR = 2 * WJ, RI = 64 / LR, IT = 16 / RI;  // lanes to a row of 16 WJ columns, rows at a time
+    const int m = lane % LR, n8 = t.nj - (c0 + 8 * m), col = t.j0 + c0 + 8 * m;
+    // Behind conditions the loads would wait for one another (6002 rows, 8 experts of 4096 x 14336: 735 -> 803 us), so they are
+    // unconditional: 8 columns that end past the row are its last 8, moved down afterwards (whole: the rows end on 8 columns, and
+    // there are none).  Rows of less than 8 are read one by one.
+    auto rows = [&](auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      const int from = min(col, a.K - 8);
       Eight g[IT], u[IT];
       auto fetch = [&](int i, int k) {
-        const unsigned r = min(32 * i + wi * 16 + k * RI + lane / LR, t.ni - 1), q = (r * (unsigned)ldg + safe) * EB;
-        g[k].load(gu, q);
-        u[k].load(gu + up, q);
+        const unsigned r = min(32 * i + wi * 16 + k * RI + lane / LR, t.ni - 1);
+        if (!WHOLE && a.K < 8) {
+          g[k].load_some(gu, r * (unsigned)ldg * EB, n8);
+          u[k].load_some(gu + up, r * (unsigned)ldg * EB, n8);
+        } else {
+          g[k].load(gu, (r * (unsigned)ldg + from) * EB);
+          u[k].load(gu + up, (r * (unsigned)ldg + from) * EB);
+        }
       };
 #pragma unroll
       for (int k = 0; k < IT; ++k) fetch(0, k);
@@ -707,6 +717,9 @@ struct TileKernel {
           const int rr = k * RI + lane / LR, r = 32 * i + wi * 16 + rr;
           float dh[8], dg[8], du[8], hv[8];
           region_row(reg, rr, m, 0, dh);
+          if constexpr (!WHOLE) {
+            if (a.K >= 8 && col > from) g[k].shift(min(col - from, 8)), u[k].shift(min(col - from, 8));
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float gv = g[k].get(e), uv = u[k].get(e), s = sigmoid(gv), gs = gv * s;
@@ -715,31 +728,16 @@ struct TileKernel {
             hv[e] = gs * uv;
           }
           fetch(min(i + 1, NI - 1), k);
-          if (r >= t.ni || col >= t.nj) continue;
+          if (r >= t.ni || n8 <= 0) continue;
           const unsigned q = (r * (unsigned)ldg + col) * EB;
-          Eight::store(dgu, q, dg);
-          Eight::store(dgu + up, q, du);
-          if (h) Eight::store(h, (unsigned)(r * (unsigned)a.K + col) * EB, hv);
+          Eight::store(dgu, q, WHOLE ? 8 : n8, dg);
+          Eight::store(dgu + up, q, WHOLE ? 8 : n8, du);
+          if (h) Eight::store(h, (unsigned)(r * (unsigned)a.K + col) * EB, WHOLE ? 8 : n8, hv);
         }
       }
-    } else {
-      if constexpr (!STAGED) wait_loads<0>();
-#pragma unroll 1
-      for (int i = 0; i < NI; ++i) {
-        acc_to_region<NI>(reg, lane, acc, i);
-        const int r0 = 32 * i + wi * 16;
-#pragma unroll 1
-        for (int r = 0; r < min(t.ni - r0, 16); ++r)
-#pragma unroll 1
-          for (int c = lane; c < min(t.nj - c0, 16 * WJ); c += 64) {
-            const size_t q = (size_t)(r0 + r) * ldg + c0 + c;
-            const float dh = region_one(reg, r, c, 0), gv = load1(gu, q), uv = load1(gu + up, q), s = sigmoid(gv), gs = gv * s;
-            store_out(dgu, q, dh * uv * (s * (1.f + gv * (1.f - s))), EB == 2);
-            store_out(dgu + up, q, dh * gs, EB == 2);
-            if (h) store_out(h, (size_t)(r0 + r) * a.K + c0 + c, gs * uv, EB == 2);
-          }
-      }
-    }
+    };
+    if (a.K % 8 == 0) rows(std::true_type{});
+    else rows(std::false_type{});
   }
 
   // One tile with NI row fragments per wave.  Its first NB stages have landed for this wave (STAGED: feed is

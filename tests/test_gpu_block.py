@@ -30,6 +30,7 @@ GROUPS = {
     "ragged": ([17, 0, 64, 1, 130], 96, 160),
     "odd": ([65, 300, 0, 1], 131, 77),
     "by8": ([33], 40, 264),
+    "by4": ([29, 150], 36, 44),
     "tiles": ([513, 255, 256, 257], 264, 200),
     "large": ([700, 1100], 1160, 648),
     "decode": ([1, 0, 2, 1, 0, 3, 9], 352, 2880),
