@@ -6,6 +6,8 @@
 // G-th chunk in 64 bits (they cost less than the bytes, the sum is as good as exact, and no square overflows) and leaves one
 // partial sum; every workgroup of the second adds those up in the same order, so all of them scale by the same number and
 // results are bitwise reproducible.
+//
+// Measured: 2^30 bf16 elements in 3 tensors 370 + 815 us (6.4 GB at 5.4 TB/s); 131,072 fp32 elements in 5 tensors 3.7 + 4.9 us.
 #include <algorithm>
 
 #include "ffn_common.hpp"
