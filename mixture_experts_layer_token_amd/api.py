@@ -607,8 +607,8 @@ def moe_grad_norm(grads, norm, ws=None, stream=None):
 
 
 def moe_clip_grad_norm(grads, max_norm, norm, outs=None, ws=None, stream=None):
-    """moe_grad_norm, then every gradient times min(1, max_norm / norm): in place, or into the tensors of `outs` (same types,
-    shapes and strides; None among them: not written).  A norm that is not finite scales nothing."""
+    """moe_grad_norm, then every gradient times min(1, max_norm / norm): in place, or into the tensors of `outs` (same types and
+    sizes, in the same order in memory; None among them: not written).  A norm that is not finite scales nothing."""
     if outs is None:
         outs = grads
     elif len(outs) != len(grads):

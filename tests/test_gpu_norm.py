@@ -253,6 +253,8 @@ LISTS = {
     "one": [1],
     "empty-among": [0, 5, 0, 8192, 3],
     "chunks": [8191, 8192, 8193, 16384, 16385, 1, 100000],
+    "sixteen-chunks": [2048] * 10 + [2047, 4095, 1, 0, 7, 2048],
+    "seventeen-chunks": [2048] * 15 + [2049],
     "many": [1 + (i * 7919) % 3000 for i in range(250)],
     "large": [30_000_001, 5, 7_000_000],
     "none": [],
