@@ -71,6 +71,30 @@ bool few_rows_kernel(int type, bool staged, int rows, int N, int E) {
   return tiles * (mean + (staged ? 16 : 4)) <= 2200;
 }
 
+// Whether the gradient through the gate runs on the kernel of small workgroups that split its sum (for `tiles` of 128 x 128).  Their
+// number is an estimate, as row counts are known on average only.  Measured, this kernel against the tile kernel (us; weights not in
+// a cache; rows x H x I, workgroups):
+//   bf16   while they fit the card at once.  40 x 4096 x 4096 (96) 20 : 29, 400 x 4096 x 768 (150) 20 : 35, 200 x 4096 x 2048 (208) 20 : 35,
+//          8 rows to 8 experts of 2880 x 2880 (184) 31 : 49;  400 to 16 experts of 2048 x 768 (198) 22 : 18, 256 to 8 of 4096 x 2048 (320)
+//          58 : 42
+//   rows through registers (staged), whose tiles wait longer for their loads:  40 x 4095 x 4095 (96) 41 : 112, 1000 x 4099 x 519 (315)
+//          69 : 124, 512 to 8 experts of 4095 x 2047 (576) 121 : 136, 8520 to 46 of 2874 x 32 (555) 39 : 79;  16 to 128 of 2880 x 2881
+//          (368) 80 : 76, 32 to 128 (736) 124 : 145, 2574 to 59 of 959 x 600 (953) 58 : 41
+//   fp32   (bound by the matrix cores, which a tile of few rows keeps as busy as a full one)   64 x 2880 x 2880 (180) 25 : 102, 300 x 4096 x
+//          4096 (1216, 96 tiles) 125 : 255, 1024 rows to 32 experts of 2048 x 2048 (2560, 512 tiles) 170 : 156, 700 x 4096 x 4096 (2816, 192
+//          tiles) 269 : 266, 400 to 8 of 64 x 4096 (1856, 256 tiles) 21 : 15;  sums over 128
+//          rows or less leave waves without work: 360 to 235 of 48 x 2496 (9165, 4700 tiles) 84 : 66, but 60 x 64 x 4096 (256) 9.5 : 12.2
+bool few_rows_gradient(const GroupArgs& a, int type, bool staged, double avg, double tiles) {
+  const int eb = type == kF32 ? 4 : 2;
+  const long long strips = (a.K * eb + kGluDxBytes - 1) / kGluDxBytes;
+  if (a.K * eb < 16 || a.ldw * eb >= 1LL << 31) return false;  // (its loads and addresses)
+  if (group_tiles_max(a.rows, a.E, kGluDxRows) * strips > kMaxThreads / kGluDxThreads) return false;
+  const double per = a.E == 1 ? std::ceil(avg / kGluDxRows) : std::max(1.0, avg / kGluDxRows + 0.5);
+  const double groups = std::min(a.rows, a.E) * per * (double)strips, cus = cu_count();
+  if (type == kF32) return groups <= 4.8 * std::max(tiles, cus) && (a.N > 128 || groups <= 3 * cus);
+  return groups <= (staged ? 3 : 0.875) * cus;
+}
+
 // The tile shape that takes the least time, from rounds of tiles and stages of 128 bytes (us; fitted to measured calls).
 // A 256 x 256 tile has a compute unit to itself: 1.46 per stage of full tiles, 10 to begin and end; 128 x 128 ones go two
 // to a compute unit, 0.94 and 7; where they leave units idle anyway, four stages in LDS instead of two hide the loads
@@ -134,6 +158,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     const double ni = op == kOpDw ? (double)((a.N + b - 1) / b) : a.E == 1 ? (double)((a.rows + b - 1) / b) : std::max(1.0, avg / b + 0.5);
     return ni * a.E * ((nj + b - 1) / b);
   };
+  if (op == kOpGluDx && few_rows_gradient(a, type, t == kStaged, avg, tiles(128))) return launch_gludx_few(a, type, s);
   // (fp32 has tiles of 128 x 128 only, with two stages, whatever shape is chosen: the order below by the chosen shape's tiles or
   // by its own took the same time to 1%)
   if (t == kLarge) t = cheapest_shape(a, op, eb, tiles(256), tiles(128), op == kOpDw ? 256 : std::min(avg, 256.0));

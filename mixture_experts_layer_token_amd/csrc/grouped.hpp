@@ -151,6 +151,10 @@ constexpr int kDecodeRows = 64;  // rows of a workgroup there
 // grouped_decode.hip: forward for few rows; direct: rows on 16-byte boundaries and spans that fit
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s);
 int launch_glu_decode(const GroupArgs& a, int type, bool direct, hipStream_t s);
+// the gradient through the gate for few rows: kGluDxRows rows and kGluDxBytes of columns to a workgroup; K of at least 16 bytes, rows of
+// w under 2 GiB, and at most kMaxThreads
+constexpr int kGluDxRows = 16, kGluDxBytes = 256, kGluDxThreads = 512;
+int launch_gludx_few(const GroupArgs& a, int type, hipStream_t s);
 // the kernel that suits the call; ws holds grouped_workspace bytes
 int launch_grouped(const GroupArgs& a, int op, int type, void* ws, hipStream_t s);
 size_t grouped_workspace(int type, int rows, int N, int K, int E);

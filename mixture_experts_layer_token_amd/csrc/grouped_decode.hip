@@ -1,4 +1,4 @@
-// Forward product grouped by expert for few rows: every touched weight is read once and nothing is reused, so
+// Forward product grouped by expert, gated block and its gradient, for few rows: every touched weight is read once and nothing is reused, so
 // the kernel is bound by the weights' bytes and, for the smallest calls, by latency.
 //
 // A workgroup computes 16 output features of up to 64 rows of one expert: many small workgroups (N / 16 per expert)
@@ -26,6 +26,7 @@ __device__ __forceinline__ f32x4 mma(const f32x4& b, const f32x4& a, f32x4 c) {
 }
 
 constexpr int kDecodeCols = 16;
+constexpr int kGluDxWaves = kGluDxThreads / 64;
 
 // Rows of 16 bytes per lane, at byte c of the row: through a buffer descriptor (DIRECT), whose end turns everything
 // outside into zeros, or by ordinary loads at any address.
@@ -222,8 +223,133 @@ int glu_launch(const GroupArgs& a, bool direct, hipStream_t s) {
   return 2 * strips <= cu_count() ? decode_launch<TYPE, kHalves>(a, direct, s) : decode_launch<TYPE, kStrips>(a, direct, s);
 }
 
+// The gradient through the gate where the tile kernel would have few tiles, or tiles of few rows: a workgroup computes 16 rows of one
+// expert by 256 bytes of columns, and its 8 waves split the long sum over the matrix rows among them, 64 bytes of every row of dy at
+// a time.  A lane loads 16 bytes of as many neighbouring matrix rows as an MFMA operand has elements per lane and turns that square
+// by itself: element c of them all is the operand whose column is the lane's own c-th.  So a wave reads the matrix in rows of 256
+// bytes, nothing passes through LDS but the waves' sums, and a lane ends with neighbouring columns.  Bound by what one compute unit
+// can read (65 GB/s) where workgroups are few, else by the matrix's bytes: 2 rows to each of 32 experts of 6524 x 896, bf16, 61 us
+// (5.3 TB/s), 16 rows x 5216 x 275, 14 experts, fp32, 40 us (the tile kernel: 132 and 259).  Deeper pipelines (3 or 4 groups of
+// loads under way instead of 2), 16 waves, or 32 rows to a workgroup took the same time or more.
+template <int TYPE>
+__device__ __forceinline__ void gludx_few_body(const GroupArgs& a, int e, int p0, int rows, int j0, float (*part)[4][64][16 / TileT<TYPE>::EB]) {
+  typedef TileT<TYPE> TT;
+  typedef typename TT::Frag Frag;
+  constexpr int EB = TT::EB, C = 16 / EB, KS = 4 * C, D = 2;  // C: columns of a lane, and matrix rows of its operand
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
+  const int len = a.N * EB, ng = (a.N + KS - 1) / KS;
+  const unsigned step = (unsigned)(a.ldw * EB);
+  // (the columns of a lane past the row's end are the row's last ones, which the lane before computes and stores alike)
+  const gptr w = (gptr)a.w + ((size_t)e * a.w_stride + min(j0 + C * (lane & 15), a.K - C)) * EB;
+  Rows<EB, false> Y;
+  Y.init((gptr)a.y, 0, (long long)(p0 + min(lane & 15, rows - 1)) * a.ldy * EB, len);
+  struct Group {
+    u32x4 w[C], y;
+  };
+  auto load = [&](Group& G, int g) {
+#pragma unroll
+    for (int r = 0; r < C; ++r) G.w[r] = load_any(w + (size_t)(unsigned)min(g * KS + q * C + r, a.N - 1) * step);
+    G.y = Y.load(g * 64 + q * 16, g * 64 + 64 <= len, len);
+  };
+  f32x4 acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = f32x4{};
+  Group ring[D];
+  constexpr int nw = kGluDxWaves;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(ring[d], wave + d * nw);
+  for (int g = wave; g < ng; g += D * nw) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      Group& G = ring[d];
+      const int at = g + d * nw;
+      // (dy is zeros there already, but zero times a matrix row that is not finite is not)
+      if (at * KS + KS > a.N) {
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+          if (at * KS + q * C + r >= a.N) G.w[r] = u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        u32x4 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (EB == 2)
+            f[i] = __builtin_amdgcn_perm(G.w[(2 * i + 1) % C][c / 2 % 4], G.w[2 * i % C][c / 2 % 4], c % 2 ? 0x07060302 : 0x05040100);
+          else
+            f[i] = G.w[i][c % 4];
+        }
+        acc[c] = mma(__builtin_bit_cast(Frag, G.y), __builtin_bit_cast(Frag, f), acc[c]);
+      }
+      load(ring[d], at + D * nw);
+    }
+  }
+  // the waves' sums in wave order, then the gate: a thread takes a lane's C columns of one row
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[wave][r][lane][c] = acc[c][r];
+  __syncthreads();
+  const int r = threadIdx.x >> 6, row = 4 * q + r, col = j0 + C * (lane & 15);
+  if (r >= 4 || row >= rows || col >= a.K) return;
+  float dh[C] = {};
+  for (int o = 0; o < nw; ++o)
+#pragma unroll
+    for (int c = 0; c < C; ++c) dh[c] += part[o][r][lane][c];
+  const size_t p = (size_t)(p0 + row), at = (p * 2 * a.K + min(col, a.K - C)) * EB, up = (size_t)a.K * EB;
+  const u32x4 gv = load_any((gptr)a.gu + at), uv = load_any((gptr)a.gu + at + up);
+  u32x4 dg = {}, du = {}, h = {};
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    auto get = [&](const u32x4& v) {
+      if constexpr (EB == 2) return __uint_as_float(c % 2 ? v[c / 2 % 4] & 0xFFFF0000u : v[c / 2 % 4] << 16);
+      return __uint_as_float(v[c % 4]);
+    };
+    auto put = [&](u32x4& v, float f) {
+      if constexpr (EB == 2) v[c / 2 % 4] |= (unsigned)f32_to_bf16_rne(f) << (c % 2 * 16);
+      else v[c % 4] = __float_as_uint(f);
+    };
+    const float g = get(gv), u = get(uv), s = 1.f / (1.f + expf(-g)), gs = g * s;
+    put(dg, dh[c] * u * (s * (1.f + g * (1.f - s))));
+    put(du, dh[c] * gs);
+    put(h, gs * u);
+  }
+  auto store = [](void* base, size_t off, const u32x4& v) {
+    typedef u32x4 __attribute__((aligned(1))) any4;
+    *(__attribute__((address_space(1))) any4*)((__attribute__((address_space(1))) char*)base + off) = v;
+  };
+  store(a.dgu, at, dg);
+  store(a.dgu, at + up, du);
+  if (a.h) store(a.h, (p * a.K + min(col, a.K - C)) * EB, h);
+}
+
+// (128 registers, two workgroups to a unit: 644 rows, 74 experts of 95 x 5784, bf16, 77 -> 64 us)
+template <int TYPE>
+__global__ __launch_bounds__(kGluDxThreads, 4) void gludx_few_kernel(GroupArgs a) {
+  constexpr int COLS = kGluDxBytes / TileT<TYPE>::EB;
+  __shared__ __align__(16) float part[kGluDxWaves][4][64][COLS / 16];
+  const int ncol = (a.K + COLS - 1) / COLS;
+  const GroupScan sc = scan_groups(a.offsets, a.E, a.rows, kGluDxRows, ncol, 0, 1);
+  if ((int)blockIdx.x >= sc.total) return;
+  const GroupSpan g = sc.find(a.offsets, a.E, a.rows, blockIdx.x);
+  const int tile = g.tile / ncol, r0 = tile * kGluDxRows;
+  gludx_few_body<TYPE>(a, g.e, g.p0 + r0, min(kGluDxRows, g.n - r0), (g.tile - tile * ncol) * COLS, part);
+}
+
+template <int TYPE>
+int gludx_few_launch(const GroupArgs& a, hipStream_t s) {
+  constexpr int COLS = kGluDxBytes / TileT<TYPE>::EB;
+  const long long nb = group_tiles_max(a.rows, a.E, kGluDxRows) * ((a.K + COLS - 1) / COLS);  // (the caller checked it)
+  hipLaunchKernelGGL(gludx_few_kernel<TYPE>, dim3((unsigned)nb), dim3(kGluDxThreads), 0, s, a);
+  MOE_CHECK_LAUNCH("moe_grouped_swiglu_dx launch");
+  return MOE_OK;
+}
+
 }  // namespace
 
+int launch_gludx_few(const GroupArgs& a, int type, hipStream_t s) {
+  return type == kF32 ? gludx_few_launch<kF32>(a, s) : gludx_few_launch<kBf16>(a, s);
+}
 int launch_grouped_decode(const GroupArgs& a, int type, bool direct, hipStream_t s) {
   return type == kI8 ? decode_launch<kI8>(a, direct, s)
                      : type == kF32 ? decode_launch<kF32>(a, direct, s) : decode_launch<kBf16>(a, direct, s);

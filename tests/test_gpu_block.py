@@ -39,6 +39,10 @@ GROUPS = {
     "many": ([i % 5 for i in range(70)], 64, 96),
     "most": ([i % 3 for i in range(1024)], 16, 32),
     "deep": ([400, 600], 128, 2048),
+    # (gradients of many tiles: the ones above are few, and have a kernel of their own)
+    "deep-wide": ([400, 600], 1024, 2048),
+    "odd-wide": ([900, 0, 700, 131], 1131, 77),
+    "by4-wide": ([640, 1111], 1132, 44),
 }
 
 
@@ -197,7 +201,7 @@ def test_gradient(name, dt, with_h):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("layout,spare,shift", [("padded", 7, 0), ("shifted", 5, 1), ("dense", 3, 1), ("dense", 0, 4)])
-@pytest.mark.parametrize("name", ["ragged", "odd", "decode", "tiles"])
+@pytest.mark.parametrize("name", ["ragged", "odd", "decode", "tiles", "odd-wide", "by4-wide"])
 def test_gradient_strides_spare_rows(name, dt, layout, spare, shift):
     say("block gradient strided", name, dt, layout, "shift", shift)
     check_gradient(make(name, DTS[dt], layout, False, spare, seed=3), DTS[dt], shift=shift, what="%s %s" % (name, layout))
@@ -226,7 +230,7 @@ def test_gradient_against_differences(dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("name", ["ragged", "odd", "tiles", "decode"])
+@pytest.mark.parametrize("name", ["ragged", "odd", "tiles", "decode", "decode-odd", "odd-wide"])
 def test_values_that_are_not_finite_stay_in_their_rows(name, dt):
     a = make(name, DTS[dt], spare=9, seed=5)
     b = make(name, DTS[dt], spare=9, seed=5)
