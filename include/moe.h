@@ -481,7 +481,9 @@ int moe_swiglu_grad(const void* gu, const void* dh, int dt, int rows, int I, con
  *   moe_norm       y = xh weight + bias,  stats[r] = {mean, rstd} unless NULL
  *   moe_norm_grad  v = dy weight,  dx = rstd (v - sum v / H (RMS: 0) - xh sum(v xh) / H) (+ add[r] unless NULL: the
  *                  residual's gradient),  dweight = sum over rows of dy xh,  dbias = sum over rows of dy
- * fp32 arithmetic, one rounding of each result; no atomics: results are bitwise reproducible.
+ * fp32 arithmetic, one rounding of each result; no atomics: results are bitwise reproducible.  moe_norm takes finite rows of any
+ * size (sums that leave fp32's range are taken of the row times a power of two); the gradient those whose deviations from the mean
+ * and whose rstd, which it reads from stats, are within fp32's normal range.
  *   x, y, dy, dx, add device [rows][H] of type dt (ldx between rows of x, ldy between those of y or dy; dx and add contiguous);
  *   weight, bias, dweight, dbias device [H] of type pdt; weight NULL: ones, bias NULL: zeros; dweight or dbias NULL: not
  *   asked for (zeros where there are no rows); stats device [rows][2] fp32

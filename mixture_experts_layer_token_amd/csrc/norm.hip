@@ -167,11 +167,82 @@ __device__ __forceinline__ void row_sums(float& s1, float& s2, float (&part)[2][
 
 // ------------------------------------------------------------------ forward
 
+// Finite rows can leave fp32's range: sums of elements from 2^108 on and squares of deviations from 2^54 on may overflow, squares below
+// 2^-126 lose bits and then vanish.  The sums of such a row are taken again, of its elements times a power of two, which is exact where
+// it counts.  var_eps is the row's variance plus eps; the result is 1 where that is right.
+//   Not finite: an element is 2^54 or more.  Times 2^-80 neither sums (2^20 elements below 2^48) nor squares overflow, and squares that
+//   vanish are nothing to the row's.  (Rows that hold a NaN or an infinity are taken again too, and stay what they were.)
+//   Below 2^-100: no deviation is more than 2^-40.  Times 2^90 the square of the smallest element is 2^-118.  Where the mean is far
+//   from that, deviations are zeros, and the variance is as it was.
+// In between, lost bits are 2^-149 to a sum of 2^-100 or more.
+
+// How far var_eps is past 2^-100, counted in floats: kOut and more if it is out of range (below it as well)
+constexpr unsigned kOut = 0x7F800000u - 0x0D800000u;
+__device__ __forceinline__ unsigned past_low(float var_eps) { return __float_as_uint(var_eps) - 0x0D800000u; }
+__device__ __forceinline__ float other_scale(float var_eps, float mean) {
+  if (past_low(var_eps) < kOut) return 1.f;
+  if (!(var_eps < 0x1p-100f)) return 0x1p-80f;
+  return fabsf(mean) < 0x1p10f ? 0x1p90f : 1.f;
+}
+
+// mean of a row times `scale` and the sum of its squared deviations, read from memory by WPR waves
+struct RowSums {
+  float mean, sq;
+};
+template <bool BF16, int WPR>
+__device__ __forceinline__ RowSums row_again(const NormArgs& a, long long r, int lane, float scale, float (&part)[2][WPR], int& parity) {
+  constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4;
+  const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+  const float inv = 1.f / (float)a.H;
+  float v[8], mean = 0.f, sum = 0.f, sq = 0.f;
+  if (!a.rms) {
+    for (int j = lane * 8; j < a.H; j += LPR * 8) {
+      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i] * scale;
+    }
+    mean = row_sum<WPR>(sum, part[parity]) * inv, parity ^= 1;
+  }
+  for (int j = lane * 8; j < a.H; j += LPR * 8) {
+    unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = j + i < a.H ? v[i] * scale - mean : 0.f;
+      sq = fmaf(d, d, sq);
+    }
+  }
+  sq = row_sum<WPR>(sq, part[parity]);
+  parity ^= 1;
+  return RowSums{mean, sq};
+}
+// its results
+template <bool BF16, int WPR>
+__device__ __forceinline__ void write_again(const NormArgs& a, long long r, int lane, float scale, RowSums s) {
+  constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4;
+  const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
+  char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
+  // 1 / sqrt(variance + eps) of the row times `scale`, and of the row.  (Without deviations eps is all there is, and any factor of
+  // theirs will do.)
+  const float inv = 1.f / (float)a.H, e = s.sq == 0.f ? 1.f : scale;
+  const float scaled = 1.f / sqrtf(fmaf(s.sq, inv, a.eps * e * e)), rstd = scaled * e;
+  float v[8], w[8], b[8];
+  for (int j = lane * 8; j < a.H; j += LPR * 8) {
+    unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
+    load_param(a.weight, a.par_bf16, j, a.H, 1.f, w);
+    load_param(a.bias, a.par_bf16, j, a.H, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] * scale - s.mean) * scaled, w[i], b[i]);
+    store_chunk<BF16>(yr, j, a.H, v);
+  }
+  if (a.stats && lane == 0) a.stats[2 * r] = s.mean / scale, a.stats[2 * r + 1] = rstd;
+}
+
 // WPR waves to a row, CH chunks of 8 elements per lane; workgroups walk over the rows, with the next row's loads under
 // way while one is worked on (a row's two sums each wait for all of its waves).
 template <bool BF16, int WPR, int CH>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs a) {
   constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, RPB = WPR > 4 ? 1 : 4 / WPR;
+  static_assert(WPR == 1 || RPB == 1, "a row that is taken again meets no other row's waves at its barriers");
   __shared__ float part[RPB][2][WPR];
   const int lane = threadIdx.x % LPR, team = __builtin_amdgcn_readfirstlane(threadIdx.x / LPR);
   const long long step = (long long)gridDim.x * RPB;
@@ -193,8 +264,13 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
   }
   const float inv = 1.f / (float)a.H;
   int parity = 0;
+  unsigned past = 0;
   // (the workgroup's waves stay together for the barriers, whether or not their team has a row)
   for (; r0 < a.rows; r0 += step) {
+    // (Which elements exist is found out again for every row: as masks held over the loop it takes more scalar registers than
+    // there are, and reading them back costs more.)
+    int n = a.H - lane * 8;
+    asm volatile("" : "+v"(n));
     float v[CH][8];
     float mean = 0.f, sum = 0.f;
 #pragma unroll
@@ -210,14 +286,15 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
     for (int c = 0; c < CH; ++c) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[c][i] = (c * LPR + lane) * 8 + i < a.H ? v[c][i] - mean : 0.f;
+        v[c][i] = c * LPR * 8 + i < n ? v[c][i] - mean : 0.f;
         sq = fmaf(v[c][i], v[c][i], sq);
       }
     }
-    const float rstd = 1.f / sqrtf(row_sum<WPR>(sq, part[team][parity]) * inv + a.eps);
+    const float var_eps = fmaf(row_sum<WPR>(sq, part[team][parity]), inv, a.eps), rstd = 1.f / sqrtf(var_eps);
     parity ^= 1;
     const long long r = r0 + team;
     if (r >= a.rows) continue;
+    past = max(past, past_low(var_eps));
     char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -227,47 +304,28 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
     }
     if (a.stats && lane == 0) a.stats[2 * r] = mean, a.stats[2 * r + 1] = rstd;
   }
+  if ((unsigned)__builtin_amdgcn_readfirstlane(past) < kOut) return;  // (the same for all waves of a row)
+  // The rare rows out of fp32's range are found by the same sums and written again, behind the loop: inside it, registers kept for them
+  // cost 8192 rows of 7168 20%.
+#pragma unroll 1
+  for (long long r = (long long)blockIdx.x * RPB + team; r < a.rows; r += step) {
+    const RowSums s = row_again<BF16, WPR>(a, r, lane, 1.f, part[team], parity);
+    const float scale = other_scale(fmaf(s.sq, inv, a.eps), s.mean);
+    if (scale != 1.f) write_again<BF16, WPR>(a, r, lane, scale, row_again<BF16, WPR>(a, r, lane, scale, part[team], parity));
+  }
 }
 
 // Rows too long for the registers: the row is read again for every sum and for the result (from L2, as it was just read).
 template <bool BF16>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
-  constexpr int LPR = 1024, EB = BF16 ? 2 : 4;
   __shared__ float part[2][16];
-  const int lane = threadIdx.x;
   const float inv = 1.f / (float)a.H;
   int parity = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const char* xr = (const char*)a.x + (size_t)r * a.ldx * EB;
-    char* yr = (char*)a.y + (size_t)r * a.ldy * EB;
-    float v[8], w[8], b[8], mean = 0.f, sum = 0.f, sq = 0.f;
-    if (!a.rms) {
-      for (int j = lane * 8; j < a.H; j += LPR * 8) {
-        unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += v[i];
-      }
-      mean = row_sum<16>(sum, part[parity]) * inv, parity ^= 1;
-    }
-    for (int j = lane * 8; j < a.H; j += LPR * 8) {
-      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = j + i < a.H ? v[i] - mean : 0.f;
-        sq = fmaf(d, d, sq);
-      }
-    }
-    const float rstd = 1.f / sqrtf(row_sum<16>(sq, part[parity]) * inv + a.eps);
-    parity ^= 1;
-    for (int j = lane * 8; j < a.H; j += LPR * 8) {
-      unpack<BF16>(load_raw<BF16>(xr, j, a.H), j, a.H, v);
-      load_param(a.weight, a.par_bf16, j, a.H, 1.f, w);
-      load_param(a.bias, a.par_bf16, j, a.H, 0.f, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - mean) * rstd, w[i], b[i]);
-      store_chunk<BF16>(yr, j, a.H, v);
-    }
-    if (a.stats && lane == 0) a.stats[2 * r] = mean, a.stats[2 * r + 1] = rstd;
+    RowSums s = row_again<BF16, 16>(a, r, threadIdx.x, 1.f, part, parity);
+    const float scale = other_scale(fmaf(s.sq, inv, a.eps), s.mean);
+    if (scale != 1.f) s = row_again<BF16, 16>(a, r, threadIdx.x, scale, part, parity);
+    write_again<BF16, 16>(a, r, threadIdx.x, scale, s);
   }
 }
 
