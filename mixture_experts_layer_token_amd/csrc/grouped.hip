@@ -71,28 +71,43 @@ bool few_rows_kernel(int type, bool staged, int rows, int N, int E) {
   return tiles * (mean + (staged ? 16 : 4)) <= 2200;
 }
 
-// Whether the gradient through the gate runs on the kernel of small workgroups that split its sum (for `tiles` of 128 x 128).  Their
-// number is an estimate, as row counts are known on average only.  Measured, this kernel against the tile kernel (us; weights not in
-// a cache; rows x H x I, workgroups):
-//   bf16   while they fit the card at once.  40 x 4096 x 4096 (96) 20 : 29, 400 x 4096 x 768 (150) 20 : 35, 200 x 4096 x 2048 (208) 20 : 35,
-//          8 rows to 8 experts of 2880 x 2880 (184) 31 : 49;  400 to 16 experts of 2048 x 768 (198) 22 : 18, 256 to 8 of 4096 x 2048 (320)
-//          58 : 42
-//   rows through registers (staged), whose tiles wait longer for their loads:  40 x 4095 x 4095 (96) 41 : 112, 1000 x 4099 x 519 (315)
-//          69 : 124, 512 to 8 experts of 4095 x 2047 (576) 121 : 136, 8520 to 46 of 2874 x 32 (555) 39 : 79;  16 to 128 of 2880 x 2881
-//          (368) 80 : 76, 32 to 128 (736) 124 : 145, 2574 to 59 of 959 x 600 (953) 58 : 41
-//   fp32   (bound by the matrix cores, which a tile of few rows keeps as busy as a full one)   64 x 2880 x 2880 (180) 25 : 102, 300 x 4096 x
-//          4096 (1216, 96 tiles) 125 : 255, 1024 rows to 32 experts of 2048 x 2048 (2560, 512 tiles) 170 : 156, 700 x 4096 x 4096 (2816, 192
-//          tiles) 269 : 266, 400 to 8 of 64 x 4096 (1856, 256 tiles) 21 : 15;  sums over 128
-//          rows or less leave waves without work: 360 to 235 of 48 x 2496 (9165, 4700 tiles) 84 : 66, but 60 x 64 x 4096 (256) 9.5 : 12.2
-bool few_rows_gradient(const GroupArgs& a, int type, bool staged, double avg, double tiles) {
+// Whether the gradient through the gate runs on the kernel of small workgroups that split its sum.  How many those and the tile
+// kernel's tiles of 128 x 128 are is an estimate, as row counts are known on average only; of E experts, as many count as rows that
+// choose at random touch.  Measured at some 800 sizes, this kernel against the tile kernel (us; weights not in a cache; rows x H x I,
+// workgroups):
+//   bf16   while they fit the card at once: then a compute unit's reading bounds each of them.  40 x 4096 x 4096 (96) 21 : 28, 400 x 4096 x
+//          768 (150) 21 : 35, 200 x 4096 x 2048 (208) 20 : 34, 100 x 4096 x 4096 (224) 21 : 35;  200 x 2880 x 2880 (299) 36 : 28.  Weights of
+//          many strips (kGluDxBytes wide) bound both kernels, the tile kernel a little less: 64 rows to 8 experts of 2880 x 2880 (184 strips)
+//          32 : 31, to 32 of 2048 x 768 (168) 25 : 23, but 8 to 128 of 2880 x 2880 (179) 25 : 34, as the tiles' shape is that for more
+//          experts than have rows.  Sums over fewer than 512 rows of the matrix leave waves without work: 9 rows to 9 experts of 64 x 1696 (82)
+//          7.6 : 6.1.  Experts of 64 rows and more make up for it: 1791 x 192 x 160 (224) 8.2 : 10.8
+//   rows through registers (staged), whose tiles wait longer for their loads, and longer in more than one round:  40 x 4095 x 4095 (96) 41 :
+//          113, 1000 x 4099 x 519 (315) 71 : 124, 400 rows to 16 experts of 4095 x 2047 (528) 96 : 128, 8510 to 46 of 2874 x 33 (555) 58 : 82;  64
+//          to 32 of 2880 x 2881 (640, as many tiles) 117 : 143, 64 to 64 of 4095 x 2047 (650) 161 : 268;  400 to 16 of 2880 x 2881 (759,
+//          half as many tiles) 112 : 80, 1767 to 45 of 63 x 625 (665) 29 : 14
+//   fp32   (bound by the matrix cores, which a tile of few rows keeps as busy as a full one)   40 x 2880 x 2880 (135) 22 : 101, 300 x 4096 x
+//          4096 (1216, 96 tiles) 126 : 259, 700 x 2880 x 2880 (1980, 138 tiles) 207 : 182.  Weights of more strips than compute units
+//          bound this kernel, and the rounds of tiles the other:  64 rows to 16 experts of 2048 x 4096 (1008, 504 tiles) 102 : 92, of
+//          2048 x 4128 (1023, 520 tiles) 99 : 145, 708 to 42 of 1776 x 3656 (3784, 1218 tiles) 315 : 237, 256 to 32 of 2880 x 2880 (1440,
+//          736 tiles) 192 : 220.  Short sums:  400 to 8 of 64 x 4096 (1856) 19 : 15, but 40 x 64 x 4096 (192) 5.8 : 11
+bool few_rows_gradient(const GroupArgs& a, int type, bool staged) {
   const int eb = type == kF32 ? 4 : 2;
-  const long long strips = (a.K * eb + kGluDxBytes - 1) / kGluDxBytes;
+  const long long width = ((long long)a.K * eb + kGluDxBytes - 1) / kGluDxBytes;
   if (a.K * eb < 16 || a.ldw * eb >= 1LL << 31) return false;  // (its loads and addresses)
-  if (group_tiles_max(a.rows, a.E, kGluDxRows) * strips > kMaxThreads / kGluDxThreads) return false;
-  const double per = a.E == 1 ? std::ceil(avg / kGluDxRows) : std::max(1.0, avg / kGluDxRows + 0.5);
-  const double groups = std::min(a.rows, a.E) * per * (double)strips, cus = cu_count();
-  if (type == kF32) return groups <= 4.8 * std::max(tiles, cus) && (a.N > 128 || groups <= 3 * cus);
-  return groups <= (staged ? 3 : 0.875) * cus;
+  if (group_tiles_max(a.rows, a.E, kGluDxRows) * width > kMaxThreads / kGluDxThreads) return false;
+  const double touched = a.E == 1 ? 1 : -a.E * std::expm1(a.rows * std::log1p(-1.0 / a.E)), avg = a.rows / touched;
+  auto count = [&](int mr) { return a.E == 1 ? std::ceil(avg / mr) : touched * std::max(1.0, avg / mr + 0.5); };
+  const double groups = count(kGluDxRows) * width, tiles = count(128) * ((a.K + 127) / 128);
+  const double strips = touched * a.K * eb / kGluDxBytes, cus = cu_count();
+  if (type == kF32) {
+    if (a.N <= 128) return groups <= 3 * cus;
+    if (staged || strips <= cus) return groups <= 4.8 * std::max(tiles, cus);
+    return groups <= 3 * cus * std::ceil(tiles / (2 * cus));
+  }
+  if (avg >= 64) return groups <= (staged ? 3 : 1) * cus;
+  const double busy = std::min(1.0, a.N / 512.0);
+  if (staged) return groups <= 2.25 * busy * std::max(tiles / 2, cus);
+  return groups <= busy * cus && (a.rows < a.E || strips <= 0.45 * cus);
 }
 
 // The tile shape that takes the least time, from rounds of tiles and stages of 128 bytes (us; fitted to measured calls).
@@ -158,7 +173,7 @@ int launch_grouped(const GroupArgs& a0, int op, int type, void* ws, hipStream_t 
     const double ni = op == kOpDw ? (double)((a.N + b - 1) / b) : a.E == 1 ? (double)((a.rows + b - 1) / b) : std::max(1.0, avg / b + 0.5);
     return ni * a.E * ((nj + b - 1) / b);
   };
-  if (op == kOpGluDx && few_rows_gradient(a, type, t == kStaged, avg, tiles(128))) return launch_gludx_few(a, type, s);
+  if (op == kOpGluDx && few_rows_gradient(a, type, t == kStaged)) return launch_gludx_few(a, type, s);
   // (fp32 has tiles of 128 x 128 only, with two stages, whatever shape is chosen: the order below by the chosen shape's tiles or
   // by its own took the same time to 1%)
   if (t == kLarge) t = cheapest_shape(a, op, eb, tiles(256), tiles(128), op == kOpDw ? 256 : std::min(avg, 256.0));
