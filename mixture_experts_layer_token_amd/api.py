@@ -528,6 +528,11 @@ def _own_ws(ws, need, device, stream):
     return ws, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
 
 
+def _steps(t):
+    """The strides that decide where elements lie."""
+    return [step for step, n in zip(t.stride(), t.shape) if n != 1]
+
+
 def _is_dense(t):
     """Whether the elements of t fill one block of memory, in whatever order of its dimensions."""
     if t.is_contiguous():
@@ -574,7 +579,7 @@ def _tensor_list(grads, outs):
         if not same:
             for i, (g, o) in enumerate(zip(grads, outs)):
                 if o is not None and (o.dtype is not g.dtype or o.shape != g.shape or not (
-                        o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride())):
+                        o.is_contiguous() and g.is_contiguous() or _steps(o) == _steps(g))):
                     raise ValueError("result %d does not have its gradient's type, size and strides" % i)
     if len(devices) > 1 or -1 in devices:
         raise ValueError("gradients and results on one GPU expected")
