@@ -511,9 +511,11 @@ int moe_norm_grad(const moe_norm_desc* d, const void* dy, const void* x, const v
 /*
  * The 2-norm over all elements of a list of gradients, and clipping by it:
  *   moe_grad_norm       norm = sqrt(sum over tensors and elements of src^2)
- *   moe_clip_grad_norm  and dst = src min(1, max_norm / norm), rounded once, for every tensor whose dst is not NULL
- * Squares and their sum are held in 64 bits; the order of the sum is fixed (bitwise reproducible, no atomics).  norm is rounded
- * to fp32.  A norm that is not finite is reported and scales nothing: dst = src.
+ *   moe_clip_grad_norm  and dst = src min(1, max_norm / norm) for every tensor whose dst is not NULL
+ * Squares and their sum are held in 64 bits; the order of the sum is fixed (bitwise reproducible, no atomics).  The factor is
+ * taken from that norm and rounded to fp32, its products to fp32 and then to the tensor's type.  norm is rounded to fp32: it is an
+ * infinity where the norm passes fp32's range, and the gradients are clipped by it all the same.  Only a NaN or an infinity among
+ * the gradients scales nothing: norm is one then, and dst = src.
  *   t     host, n entries, read during the call only (it may be captured into a graph: the addresses are then fixed)
  *   norm  device, one fp32 (out)
  *   ws    moe_grad_norm_workspace bytes (device, 256-byte aligned); one call at a time may use it

@@ -613,7 +613,8 @@ def moe_grad_norm(grads, norm, ws=None, stream=None):
 
 def moe_clip_grad_norm(grads, max_norm, norm, outs=None, ws=None, stream=None):
     """moe_grad_norm, then every gradient times min(1, max_norm / norm): in place, or into the tensors of `outs` (same types and
-    sizes, in the same order in memory; None among them: not written).  A norm that is not finite scales nothing."""
+    sizes, in the same order in memory; None among them: not written).  Gradients that hold a NaN or an infinity are not scaled; a
+    norm past fp32's range is an infinity in `norm` and scales like any other."""
     if outs is None:
         outs = grads
     elif len(outs) != len(grads):

@@ -123,7 +123,9 @@ __device__ __forceinline__ void add_squares(gptr p, int len, int tid, double (&v
   });
 }
 // The factor of a norm n: `scale`, then `post`.  A factor that fp32 holds with fewer bits is applied in two: gradients near the end
-// of the fp32 range have a norm past it.  A norm that is not finite scales nothing.
+// of the fp32 range have a norm past it.  A norm that is not finite in 64 bits is one of a NaN or an infinity, and scales nothing.
+// Factor and products are rounded to fp32, 2^-24 of the value each, where a factor in 64 bits would cost the store loop two conversions
+// per element; bf16 results are rounded by 2^-8.
 struct Factor {
   float scale, post;
   bool one;

@@ -250,7 +250,8 @@ class Norm(torch.nn.Module):
         self.bias = torch.nn.Parameter(torch.zeros(H, dtype=dtype, device=device)) if has_bias else None
 
     def with_residual(self, x):
-        """(norm(x), x): use the second for the residual, and the two gradients of x are added in the norm's own kernel."""
+        """(norm(x), x): use the second for the residual, and the two gradients of x are added in the norm's own kernel.  (A view of
+        x: not to be changed in place.)"""
         _check_rows(x, self.weight.shape[0], self.weight, self.bias)
         with torch.cuda.device(x.device):
             return _NormFunction.apply(x, self.weight, self.bias, self.eps, self.rms, _keeps(x, self.weight, self.bias))
@@ -277,8 +278,9 @@ class MoeTrainBlock(torch.nn.Module):
 
 def clip_grad_norm(parameters, max_norm):
     """Scale the gradients of `parameters` in place by min(1, max_norm / norm), where norm is the 2-norm over all of them, and
-    return norm (float32 [1], on the device: nothing waits for it).  A norm that is not finite scales nothing.  A gradient that
-    several parameters share counts once."""
+    return norm (float32 [1], on the device: nothing waits for it).  `max_norm`: positive and finite.  A NaN or an infinity among
+    the gradients scales nothing and makes norm one; a norm past fp32's range is an infinity there, and scales.  A gradient
+    that several parameters share counts once."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = list({id(p.grad): p.grad for p in parameters if p.grad is not None}.values())
     if not grads:
