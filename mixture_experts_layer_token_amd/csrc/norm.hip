@@ -9,8 +9,9 @@
 // rows stay in registers while a workgroup walks over its rows, one partial sum per workgroup goes to memory, and a second
 // kernel adds those up in order: no atomics, results are bitwise reproducible.
 //
-// Measured, bf16, inputs in no cache: 8192 rows of 7168 forward 50 us (4.7 TB/s), gradient with the residual's 86 + 5 us (5.2 TB/s;
-// the parts are 15 MB of it); 517 rows of 2880, gradient, 8.4 + 3.5 us; one row of 7168, forward, 3.1 us.
+// Measured, bf16, inputs in no cache: 8192 rows of 7168 forward 52 us (4.6 TB/s), gradient with the residual's 87 + 5 us (5.2 TB/s;
+// the parts are 15 MB of it); 517 rows of 2880, gradient, 7.5 + 3.4 us; one row of 7168, forward, 3.0 us.  fp32: 8192 rows of 7168 forward
+// 89 us (5.2 TB/s), gradient 173 + 5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -352,7 +353,7 @@ __device__ __forceinline__ void write_dx(const NormArgs& a, long long r, int j, 
 }
 
 // 1024 threads: 16 / WPR teams of WPR waves, a row to a team at a time, the next row's loads under way (one chunk per lane; two
-// leave no registers for that: spilled, it takes 136 us instead of 84 for 4000 rows of 16384).
+// leave no registers for that: spilled, it takes 136 us instead of 84 for 4000 rows of 16384; two are spilled as it is).
 template <bool BF16, int WPR, int CH>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
   constexpr int LPR = 64 * WPR, EB = BF16 ? 2 : 4, TEAMS = 16 / WPR;
